@@ -1,0 +1,544 @@
+// b8_attn.cu -- attention over the block-scaled 8-bit cache (kvq_b8_attn):
+// out = softmax(scale q K^T + causal mask) V, ragged queries.
+//
+// The rows of a (sequence, kv head) are its (query, head of the group) pairs,
+// query-major.  One CTA takes one tile of R = 8 or 16 rows and one range of
+// tokens; its 8 warps take 16-token tiles in turn, each with its own softmax
+// state (m, l, O), staged by cp.async into a ring that only this warp reads
+// (no CTA barrier inside the loop).  The states are merged once at the end;
+// ranges are merged by a second kernel.  Bound for a few rows: the codes from
+// HBM, read once.
+//   * Scores are kept in log2 units in fp32; m follows the row maximum with a
+//     slack of 8 (p up to 2^8), so O is rarely rescaled.
+//   * P enters the second product as p * v_scale / vref in fp16 (bf16 output)
+//     or as fp16 hi + lo (fp32 output), where vref is the warp's largest
+//     power-of-two bound of the block scales so far and 64 / vref keeps the
+//     products at most 2^14; l sums the unrounded p.
+#include <cuda_bf16.h>
+
+#include "b8_mma.cuh"
+
+namespace kvq {
+namespace {
+
+using namespace b8;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr float kEmpty = -1e30f;  // running maximum before any token
+constexpr float kSlack = 8.f;
+
+template <int D, int R, bool HILO>
+struct Cfg {
+  static constexpr int kTileBytes = kTok * D;           // K or V of a warp's tile
+  static constexpr int kStageBytes = 2 * kTileBytes + 16;  // + k_scale, v_scale
+  static constexpr int kCtas = D == 256 || R == 16 ? 1 : 2;  // resident per SM
+  // 128 KB of tiles in flight or landing per SM
+  static constexpr int kStages = D == 256 ? 3 : D == 128 ? (kCtas == 2 ? 3 : 5) : (kCtas == 2 ? 5 : 9);
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  // after the ring: queries, their factors and their token limits
+  static constexpr int kOffQ = kRing;
+  static constexpr int kOffInv = kOffQ + QTile<D, R, HILO>::kBytes;
+  static constexpr int kOffLim = kOffInv + R * 4;
+  static constexpr int kSmem = kOffLim + R * 4;
+  // the merge reuses the ring: per warp R x (D + 4) of O, then m, l and vref
+  static constexpr int kRow = D + 4;
+  static constexpr int kOffM = kWarps * R * kRow * 4;
+  static_assert(kOffM + kWarps * (2 * R + 1) * 4 <= kRing, "merge fits the ring");
+  static_assert(kSmem * kCtas <= 227 * 1024, "shared memory per SM");
+};
+
+struct AttnArgs {
+  kvq_b8_cache c;
+  B8Queries q;
+  B8Plan p;
+  void *out;
+  float *lse, *ws;
+  uint32_t *err;
+};
+
+template <int D, bool HILO>
+__device__ __forceinline__ void store_out(void *out, int64_t at, float4 v) {
+  if (HILO) {
+    *reinterpret_cast<float4 *>(static_cast<float *>(out) + at) = v;
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    uint2 u;
+    u.x = *reinterpret_cast<const uint32_t *>(&a);
+    u.y = *reinterpret_cast<const uint32_t *>(&b);
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at) = u;
+  }
+}
+
+// grid: split + splits * (row tile + row_tiles * (kv head + heads * sequence))
+template <int D, int R, bool HILO>
+__global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
+    b8_attn_kernel(const __grid_constant__ AttnArgs a) {
+  using C = Cfg<D, R, HILO>;
+  constexpr int kNb = R / 8;       // n blocks of the second product
+  constexpr int kMt = D / 16;      // m tiles of the second product
+  constexpr int kKs = D / 16;      // k steps of the first product
+  constexpr int kL = QTile<D, R, HILO>::kLevels;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, tg = lane & 3;
+  const kvq_b8_cache &c = a.c;
+
+  int u = blockIdx.x;
+  const int split = u % a.p.splits;
+  u /= a.p.splits;
+  const int rt = u % a.p.row_tiles;
+  u /= a.p.row_tiles;
+  const int kvh = u % c.num_kv_heads, b = u / c.num_kv_heads;
+
+  int q0;
+  const int nq = query_range(a.q, b, q0);
+  const int n_rows = nq * a.q.group, row0 = rt * R;
+  if (row0 >= n_rows) return;
+  const int len = seq_len(a.q, c, b);
+  // query i attends to tokens below len - nq + i + 1
+  const int i_last = (min(row0 + R, n_rows) - 1) / a.q.group;
+  const int hi_lim = max(0, len - nq + i_last + 1);
+  const int lo_lim = max(0, len - nq + row0 / a.q.group + 1);
+  const int t0 = split * a.p.split_tokens;
+  const int t1 = min(hi_lim, t0 + a.p.split_tokens);
+  if (t0 >= t1 && split > 0) return;  // the combine kernel knows
+
+  uint32_t *qimg = reinterpret_cast<uint32_t *>(smem + C::kOffQ);
+  float *inv_s = reinterpret_cast<float *>(smem + C::kOffInv);
+  int *lim_s = reinterpret_cast<int *>(smem + C::kOffLim);
+
+  // ---- staging of this warp's tiles: tile w of the range goes to warp w % 8
+  const int first = t0 / kTok + warp;
+  const int n_tiles = t1 > t0 ? max(0, ((t1 + kTok - 1) / kTok - first + kWarps - 1) / kWarps) : 0;
+  uint8_t *ring = smem + warp * C::kStages * C::kStageBytes;
+  const int per_block = c.block_size / kTok;
+  const int32_t *table = c.block_table + (int64_t)b * c.max_blocks_per_seq;
+  // lane l holds the block of tile page_base + l
+  int page_base = 0, page = -1;
+  auto load_pages = [&](int base) {
+    page_base = base;
+    const int col = (first + (base + lane) * kWarps) / per_block;
+    page = base + lane < n_tiles && col < c.max_blocks_per_seq ? __ldg(table + col) : -1;
+    if (page >= c.num_blocks) page = -1;
+  };
+  uint32_t live = 0;  // bit s: the tile in stage s is mapped
+  auto issue = [&](int it) {
+    const int st = it % C::kStages;
+    if (it < n_tiles) {
+      if (it >= page_base + 32) load_pages(it);
+      const int slot = __shfl_sync(0xffffffffu, page, it - page_base);
+      const int tile = first + it * kWarps;
+      const bool mapped = slot >= 0 && in_bounds(slot, slot + 1, c.num_blocks, a.err);
+      live = mapped ? live | (1u << st) : live & ~(1u << st);
+      if (mapped) {
+        const int64_t sh = (int64_t)slot * c.num_kv_heads + kvh;
+        const int64_t off = (sh * c.block_size + tile % per_block * kTok) * D;
+        const uint32_t dst = smem_u32(ring + st * C::kStageBytes);
+#pragma unroll
+        for (int i = 0; i < C::kTileBytes / 512; i++) {
+          const int ch = lane + 32 * i, r = ch / (D / 16), cc = ch % (D / 16);
+          cp_async16(dst + k_off<D>(r, cc), c.k_codes + off + 16 * ch);
+          cp_async16(dst + C::kTileBytes + v_off<D>(r, cc), c.v_codes + off + 16 * ch);
+        }
+        if (lane < 2)
+          cp_async4(dst + 2 * C::kTileBytes + 4 * lane, (lane ? c.v_scales : c.k_scales) + sh);
+      }
+    }
+    cp_commit();
+  };
+  if (n_tiles > 0) load_pages(0);
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; i++) issue(i);
+
+  stage_queries<D, R, HILO>(a.q, q0, kvh, row0, n_rows, warp, kWarps, lane, qimg, inv_s);
+  if (tid < R) lim_s[tid] = row0 + tid < n_rows ? max(0, len - nq + (row0 + tid) / a.q.group + 1) : 0;
+  __syncthreads();
+  const float inv0 = inv_s[g], inv1 = R == 16 ? inv_s[R == 16 ? g + 8 : g] : 0.f;
+  const int lim0 = lim_s[g], lim1 = R == 16 ? lim_s[R == 16 ? g + 8 : g] : 0;
+  const bool whole = row0 + R <= n_rows;
+
+  constexpr bool kQRegs = R == 8 && D <= 128;
+  uint4 qr[kQRegs ? kKs : 1];
+  if (kQRegs) {
+#pragma unroll
+    for (int ks = 0; ks < kKs; ks++)
+      qr[kQRegs ? ks : 0] = *reinterpret_cast<const uint4 *>(qimg + (ks * 32 + lane) * 4);
+  }
+
+  float o[kMt][kNb][4];
+#pragma unroll
+  for (int j = 0; j < kMt; j++)
+#pragma unroll
+    for (int n = 0; n < kNb; n++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) o[j][n][e] = 0.f;
+  float m[kNb], l[kNb];
+#pragma unroll
+  for (int n = 0; n < kNb; n++) m[n] = kEmpty, l[n] = 0.f;
+  float vref = 0x1p-100f;
+
+  for (int it = 0; it < n_tiles; it++) {
+    cp_wait<C::kStages - 2>();
+    __syncwarp();
+    issue(it + C::kStages - 1);
+    const int st = it % C::kStages;
+    if (!(live >> st & 1)) continue;
+    const uint8_t *kt = ring + st * C::kStageBytes, *vt = kt + C::kTileBytes;
+    const float ks_ = *reinterpret_cast<const float *>(kt + 2 * C::kTileBytes);
+    const float vs_ = *reinterpret_cast<const float *>(kt + 2 * C::kTileBytes + 4);
+    const int tok = (first + it * kWarps) * kTok;
+
+    // S: rows g (c0, c1) and g + 8 (c2, c3), tokens 8 n + 2 tg, + 1
+    float s[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; n++) {
+#pragma unroll
+      for (int e = 0; e < 4; e++) s[n][e] = 0.f;
+    }
+#pragma unroll
+    for (int blk = 0; blk < D / 64; blk++) {
+      uint4 kw[2];
+#pragma unroll
+      for (int n = 0; n < 2; n++)
+        kw[n] = *reinterpret_cast<const uint4 *>(kt + k_off<D>(8 * n + g, 4 * blk + tg));
+#pragma unroll
+      for (int w = 0; w < 4; w++) {
+        const int ks = 4 * blk + w;
+        uint4 qa[kL];
+        if (kQRegs) {
+          qa[0] = qr[kQRegs ? ks : 0];
+        } else {
+#pragma unroll
+          for (int v = 0; v < kL; v++)
+            qa[v] = *reinterpret_cast<const uint4 *>(qimg + ((ks * kL + v) * 32 + lane) * 4);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; n++) {
+          uint32_t b0, b1;
+          k_frag(word(kw[n], w), b0, b1);
+#pragma unroll
+          for (int v = 0; v < kL; v++) mma16816(s[n], qa[v], b0, b1);
+        }
+      }
+    }
+    // scores in log2 units, p[row block][token pair]
+    float p[kNb][4];
+    float tmax[kNb];
+#pragma unroll
+    for (int nb = 0; nb < kNb; nb++) {
+      const float f = __fmul_rn(nb ? inv1 : inv0, ks_);
+#pragma unroll
+      for (int n = 0; n < 2; n++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          float x = s[n][2 * nb + e];
+          if (R == 8 && HILO) x += s[n][2 + e];
+          p[nb][2 * n + e] = x * f;
+        }
+    }
+    if (tok + kTok > lo_lim || !whole) {
+#pragma unroll
+      for (int nb = 0; nb < kNb; nb++)
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          if (tok + 8 * (e >> 1) + 2 * tg + (e & 1) >= (nb ? lim1 : lim0)) p[nb][e] = -INFINITY;
+    }
+    bool grow = false;
+    const bool vgrow = vs_ > vref;
+#pragma unroll
+    for (int nb = 0; nb < kNb; nb++) {
+      float x = fmaxf(fmaxf(p[nb][0], p[nb][1]), fmaxf(p[nb][2], p[nb][3]));
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+      tmax[nb] = x;
+      grow |= x > m[nb] + kSlack;
+    }
+    if (__any_sync(0xffffffffu, grow) || vgrow) {
+      float vfac = 1.f;
+      if (vgrow) {
+        // power of two at or above the scale (infinite scales give NaN)
+        const uint32_t ex = (__float_as_uint(vs_) + 0x7fffffu) & 0x7f800000u;
+        const float nref = __uint_as_float(ex);
+        vfac = __fdiv_rn(vref, nref);
+        vref = nref;
+      }
+#pragma unroll
+      for (int nb = 0; nb < kNb; nb++) {
+        const float mn = tmax[nb] > m[nb] + kSlack ? tmax[nb] : m[nb];
+        const float al = ex2(m[nb] - mn);
+        l[nb] *= al;
+        m[nb] = mn;
+        // this lane's columns of O are rows 2 tg and 2 tg + 1 of the block
+        const float a0 = __shfl_sync(0xffffffffu, al, 8 * tg) * vfac;
+        const float a1 = __shfl_sync(0xffffffffu, al, 8 * tg + 4) * vfac;
+#pragma unroll
+        for (int j = 0; j < kMt; j++) {
+          o[j][nb][0] *= a0, o[j][nb][1] *= a1;
+          o[j][nb][2] *= a0, o[j][nb][3] *= a1;
+        }
+      }
+    }
+    const float vf = __fdiv_rn(vs_ * 64.f, vref);
+    uint32_t ph[kNb][2], pl[kNb][2];
+#pragma unroll
+    for (int nb = 0; nb < kNb; nb++) {
+#pragma unroll
+      for (int n = 0; n < 2; n++) {
+        const float e0 = ex2(p[nb][2 * n] - m[nb]), e1 = ex2(p[nb][2 * n + 1] - m[nb]);
+        l[nb] += e0 + e1;
+        const float2 w = make_float2(e0 * vf, e1 * vf);
+        if (HILO)
+          dec::split_hilo(w, ph[nb][n], pl[nb][n]);
+        else
+          ph[nb][n] = pack_f16x2(w.x, w.y);
+      }
+    }
+    // O^T += V^T P^T.  The k index 2 tg + {0, 1} of the fragments is token
+    // 2 tg + {0, 1}, 2 tg + 8 + {0, 1} token 8 + 2 tg + {0, 1}.
+    constexpr int kPieces = D == 64 ? 1 : D / 128;  // 16 (8) dims of each token
+#pragma unroll
+    for (int pc = 0; pc < kPieces; pc++) {
+      uint4 vw[4];
+#pragma unroll
+      for (int t = 0; t < 4; t++) {
+        const int r = 2 * tg + (t & 1) + 8 * (t >> 1);
+        if (D == 64) {
+          const uint2 x = *reinterpret_cast<const uint2 *>(vt + v_off<D>(r, g >> 1) + 8 * (g & 1));
+          vw[t] = make_uint4(x.x, x.y, 0, 0);
+        } else {
+          vw[t] = *reinterpret_cast<const uint4 *>(vt + v_off<D>(r, g + 8 * pc));
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < (D == 64 ? 2 : 4); w++) {
+        uint32_t f[4];
+#pragma unroll
+        for (int t = 0; t < 4; t++) f[t] = word(vw[t], w) ^ 0x80808080u;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {  // dims 4 w + 2 h, + 1 of the piece
+          const uint32_t x = __byte_perm(f[0], f[1], h ? 0x7362 : 0x5140);
+          const uint32_t y = __byte_perm(f[2], f[3], h ? 0x7362 : 0x5140);
+          const uint32_t fr[4] = {pair_h2(x, 0x4140), pair_h2(x, 0x4342), pair_h2(y, 0x4140),
+                                  pair_h2(y, 0x4342)};
+          const int j = (D == 64 ? 0 : 8 * pc) + 2 * w + h;
+#pragma unroll
+          for (int nb = 0; nb < kNb; nb++) {
+            mma16816(o[j][nb], fr, ph[nb][0], ph[nb][1]);
+            if (HILO) mma16816(o[j][nb], fr, pl[nb][0], pl[nb][1]);
+          }
+        }
+      }
+    }
+  }
+  cp_wait<0>();
+#pragma unroll
+  for (int nb = 0; nb < kNb; nb++) {
+    l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], 1);
+    l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], 2);
+  }
+  __syncthreads();  // every warp is done with its ring
+
+  // ---- merge of the warps' states
+  float *mo = reinterpret_cast<float *>(smem) + warp * R * C::kRow;
+  float *mm = reinterpret_cast<float *>(smem + C::kOffM);  // [warp][R]
+  float *ml = mm + kWarps * R, *mv = ml + kWarps * R;
+#pragma unroll
+  for (int nb = 0; nb < kNb; nb++) {
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+      float *row = mo + (8 * nb + 2 * tg + e) * C::kRow;
+#pragma unroll
+      for (int j = 0; j < kMt; j += 2) {
+        const int d = D == 64 ? 8 * g + 2 * j : 128 * (j >> 3) + 16 * g + 2 * (j & 7);
+        *reinterpret_cast<float4 *>(row + d) =
+            make_float4(o[j][nb][e], o[j][nb][2 + e], o[j + 1][nb][e], o[j + 1][nb][2 + e]);
+      }
+    }
+    if (tg == 0) {
+      mm[warp * R + 8 * nb + g] = m[nb];
+      ml[warp * R + 8 * nb + g] = l[nb];
+    }
+  }
+  if (lane == 0) mv[warp] = vref * 0x1p-6f;
+  __syncthreads();
+  // warp w: rows w, w + 8
+  for (int r = warp; r < R; r += kWarps) {
+    const int row = row0 + r;
+    if (row >= n_rows) break;
+    float M = kEmpty, L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) M = fmaxf(M, mm[w * R + r]);
+    float f[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+      f[w] = ex2(mm[w * R + r] - M);
+      L += f[w] * ml[w * R + r];
+      f[w] *= mv[w];
+    }
+    const bool direct = a.p.splits == 1;
+    const float norm = direct ? (L > 0.f ? __fdiv_rn(1.f, L) : L == 0.f ? 0.f : L) : 1.f;
+    const int i = row / a.q.group, head = kvh * a.q.group + row - i * a.q.group;
+    const int64_t orow = (int64_t)(q0 + i) * a.q.num_heads + head;
+    float *rec = a.ws + ((int64_t)blockIdx.x * R + r) * (D + 4);
+    for (int d = 4 * lane; d < D; d += 128) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; w++) {
+        const float4 x = *reinterpret_cast<const float4 *>(reinterpret_cast<float *>(smem) +
+                                                           (w * R + r) * C::kRow + d);
+        acc.x += f[w] * x.x, acc.y += f[w] * x.y, acc.z += f[w] * x.z, acc.w += f[w] * x.w;
+      }
+      acc.x *= norm, acc.y *= norm, acc.z *= norm, acc.w *= norm;
+      if (direct)
+        store_out<D, HILO>(a.out, orow * D + d, acc);
+      else
+        *reinterpret_cast<float4 *>(rec + 4 + d) = acc;
+    }
+    if (lane == 0) {
+      if (!direct)
+        rec[0] = M, rec[1] = L;
+      else if (a.lse != nullptr)
+        a.lse[orow] = L == 0.f ? -INFINITY : kLn2 * (M + log2f(L));
+    }
+  }
+}
+
+// One CTA per row: merge its splits' records.
+// grid: row of the tile + R * (row tile + row_tiles * (kv head + heads * sequence))
+constexpr int kCombine = 128;
+template <int D, bool HILO>
+__global__ void __launch_bounds__(kCombine) b8_combine_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int kCols = D / 4, kParts = kCombine / kCols;
+  __shared__ float part[kParts > 1 ? (kParts - 1) * D : 1];
+  __shared__ float red[2][kCombine / 32];
+  const int R = a.p.rows, tid = threadIdx.x;
+  const int r = blockIdx.x % R;
+  const int unit = blockIdx.x / R;
+  int u = unit;
+  const int rt = u % a.p.row_tiles;
+  u /= a.p.row_tiles;
+  const int kvh = u % a.c.num_kv_heads, b = u / a.c.num_kv_heads;
+  int q0;
+  const int nq = query_range(a.q, b, q0);
+  const int n_rows = nq * a.q.group, row = rt * R + r;
+  if (row >= n_rows) return;
+  const int len = seq_len(a.q, a.c, b);
+  const int i_last = (min(rt * R + R, n_rows) - 1) / a.q.group;
+  const int hi_lim = max(0, len - nq + i_last + 1);
+  const int n = max(1, (hi_lim + a.p.split_tokens - 1) / a.p.split_tokens);
+  dec::grid_dependency_wait();
+  const float *rec = a.ws + ((int64_t)unit * a.p.splits * R + r) * (D + 4);
+  const int64_t step = (int64_t)R * (D + 4);
+  float M = kEmpty;
+  for (int s = tid; s < n; s += kCombine) M = fmaxf(M, rec[s * step]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if ((tid & 31) == 0) red[0][tid >> 5] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kCombine / 32; w++) M = fmaxf(M, red[0][w]);
+  float L = 0.f;
+  for (int s = tid; s < n; s += kCombine) L += ex2(rec[s * step] - M) * rec[s * step + 1];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if ((tid & 31) == 0) red[1][tid >> 5] = L;
+  const int col = tid % kCols, pt = tid / kCols;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = pt; s < n; s += kParts) {
+    const float f = ex2(rec[s * step] - M);
+    const float4 x = *reinterpret_cast<const float4 *>(rec + s * step + 4 + 4 * col);
+    acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+  }
+  if (kParts > 1 && pt > 0)
+    *reinterpret_cast<float4 *>(part + (pt - 1) * D + 4 * col) = acc;
+  __syncthreads();
+  if (pt > 0) return;
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kCombine / 32; w++) L += red[1][w];
+#pragma unroll
+  for (int i = 0; i < kParts - 1; i++) {
+    const float4 x = *reinterpret_cast<const float4 *>(part + i * D + 4 * col);
+    acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+  }
+  const float norm = L > 0.f ? __fdiv_rn(1.f, L) : L == 0.f ? 0.f : L;
+  acc.x *= norm, acc.y *= norm, acc.z *= norm, acc.w *= norm;
+  const int i = row / a.q.group;
+  const int64_t orow = (int64_t)(q0 + i) * a.q.num_heads + kvh * a.q.group + row - i * a.q.group;
+  store_out<D, HILO>(a.out, orow * D + 4 * col, acc);
+  if (tid == 0 && a.lse != nullptr) a.lse[orow] = L == 0.f ? -INFINITY : kLn2 * (M + log2f(L));
+}
+
+template <int D, int R, bool HILO>
+cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
+  using C = Cfg<D, R, HILO>;
+  auto *k = b8_attn_kernel<D, R, HILO>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t units = (int64_t)a.q.batch * a.c.num_kv_heads * a.p.row_tiles;
+  k<<<(unsigned)(units * a.p.splits), kThreads, C::kSmem, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.p.splits == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * R));
+  cfg.blockDim = dim3(kCombine);
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, b8_combine_kernel<D, HILO>, a);
+}
+
+template <int D>
+cudaError_t by_rows(const AttnArgs &a, cudaStream_t s) {
+  if (a.p.rows == 8)
+    return a.q.bf16 ? launch<D, 8, false>(a, s) : launch<D, 8, true>(a, s);
+  return a.q.bf16 ? launch<D, 16, false>(a, s) : launch<D, 16, true>(a, s);
+}
+
+}  // namespace
+
+B8Plan plan_b8_attn(const kvq_b8_cache &c, int group, int batch, int max_q, int max_seq_len) {
+  B8Plan p;
+  const int64_t rows = (int64_t)max_q * group;
+  p.rows = rows <= 8 ? 8 : 16;
+  p.row_tiles = (int)((rows + p.rows - 1) / p.rows);
+  const int64_t units = (int64_t)batch * c.num_kv_heads * p.row_tiles;
+  const int64_t cap = (int64_t)c.max_blocks_per_seq * c.block_size;
+  const int64_t len = max((int64_t)1, min((int64_t)max_seq_len, cap));
+  // about four CTAs for each that the card holds at once, of at least 16 tiles
+  // a warp where that leaves one CTA for each
+  const int resident = kNumSMs * (c.head_dim == 256 || p.rows == 16 ? 1 : 2);
+  const int64_t granule = kWarps * kTok;
+  const int64_t most = (len + granule - 1) / granule;
+  int64_t want = (4LL * resident + units - 1) / units;
+  const int64_t full = (resident + units - 1) / units;  // splits that fill the card once
+  want = min(want, max(full, (len + 2047) / 2048));
+  want = max((int64_t)1, min(want, most));
+  int64_t tokens = (len + want - 1) / want;
+  tokens = (tokens + granule - 1) / granule * granule;
+  p.split_tokens = (int)tokens;
+  p.splits = (int)((len + tokens - 1) / tokens);
+  return p;
+}
+
+size_t b8_attn_workspace_bytes(const kvq_b8_cache &c, int batch, const B8Plan &p) {
+  if (p.splits == 1) return 0;
+  return (size_t)batch * c.num_kv_heads * p.row_tiles * p.splits * p.rows * (c.head_dim + 4) * 4;
+}
+
+cudaError_t launch_b8_attn(const kvq_b8_cache &c, const B8Queries &q, const B8Plan &p, void *out,
+                           float *lse, float *ws, cudaStream_t s) {
+  const AttnArgs a = {c, q, p, out, lse, ws, device_error_word()};
+  switch (c.head_dim) {
+    case 64: return by_rows<64>(a, s);
+    case 128: return by_rows<128>(a, s);
+    default: return by_rows<256>(a, s);
+  }
+}
+
+}  // namespace kvq

@@ -1,0 +1,68 @@
+// b8_common.cuh -- device helpers of the block-scaled 8-bit cache.  Nothing
+// here is part of the C ABI.
+#pragma once
+
+#include "b8_internal.cuh"
+
+namespace kvq {
+namespace b8 {
+
+// physical block of column `col` of sequence b; -1 if the column lies outside
+// the table or its entry outside [0, num_blocks)
+__device__ __forceinline__ int64_t block_of(const kvq_b8_cache &c, int b, int col) {
+  if (col < 0 || col >= c.max_blocks_per_seq) return -1;
+  const int p = __ldg(c.block_table + (int64_t)b * c.max_blocks_per_seq + col);
+  return p < 0 || p >= c.num_blocks ? -1 : p;
+}
+
+// amax below 2^-100 counts as 0: 1 / scale stays finite, and such values
+// vanish beside any other
+__device__ __forceinline__ float scale_of(float amax) {
+  return amax < 0x1p-100f ? 0.f : __fdiv_rn(amax, 127.f);
+}
+__device__ __forceinline__ float inverse(float scale) {
+  return scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
+}
+
+// rint(x * inv) of 4 values, clamped to [-127, 127], as packed bytes.  The sum
+// with 1.5 * 2^23 rounds to the nearest even integer and leaves it in the low
+// byte; NaN products (an infinite input times 0) come out as some code.
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  constexpr float kMagic = 12582912.f;
+  auto one = [](float x) {
+    return __float_as_uint(__fadd_rn(fminf(fmaxf(x, -127.f), 127.f), kMagic));
+  };
+  return __byte_perm(__byte_perm(one(a), one(b), 0x0040), __byte_perm(one(c), one(d), 0x0040),
+                     0x5410);
+}
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
+  return make_uint2(encode4(__fmul_rn(x[0], inv), __fmul_rn(x[1], inv), __fmul_rn(x[2], inv),
+                            __fmul_rn(x[3], inv)),
+                    encode4(__fmul_rn(x[4], inv), __fmul_rn(x[5], inv), __fmul_rn(x[6], inv),
+                            __fmul_rn(x[7], inv)));
+}
+
+// the 4 codes of a word as exact fp32 values: byte + 128 in the mantissa of
+// 2^23, less 2^23 + 128
+__device__ __forceinline__ void codes4(uint32_t w, float (&v)[4]) {
+  const uint32_t f = w ^ 0x80808080u;
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+    v[i] = __uint_as_float(__byte_perm(f, 0x4B000000u, 0x7440 + i)) - 8388736.f;
+}
+__device__ __forceinline__ void decode4(uint32_t w, float scale, float *out) {
+  float v[4];
+  codes4(w, v);
+#pragma unroll
+  for (int i = 0; i < 4; i++) out[i] = __fmul_rn(v[i], scale);
+}
+// rint(code * ratio) of 4 codes
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
+  float v[4];
+  codes4(w, v);
+  return encode4(__fmul_rn(v[0], ratio), __fmul_rn(v[1], ratio), __fmul_rn(v[2], ratio),
+                 __fmul_rn(v[3], ratio));
+}
+
+}  // namespace b8
+}  // namespace kvq

@@ -1,0 +1,55 @@
+// b8_internal.cuh -- launchers of the rotary positions and of the block-scaled
+// 8-bit cache.  Nothing here is part of the C ABI.
+#pragma once
+
+#include "kvq_internal.cuh"
+
+namespace kvq {
+
+// q, k: heads to rotate (k.num_heads 0: none); spec.d_inv_freq set
+cudaError_t launch_rope(const kvq_rope_spec &spec, int bf16, int head_dim, int num_tokens,
+                        const int32_t *positions, int inverse, const kvq_heads &q,
+                        const kvq_heads &q_out, const kvq_heads &k, const kvq_heads &k_out,
+                        cudaStream_t s);
+// spec.d_inv_freq nullptr: K is stored as it comes
+cudaError_t launch_b8_append(const kvq_b8_cache &c, const kvq_heads &k, const kvq_heads &v,
+                             int bf16, int batch, int t_new, const int32_t *start_pos,
+                             const int32_t *new_lens, const kvq_rope_spec &spec,
+                             const int32_t *rope_pos, cudaStream_t s);
+cudaError_t launch_b8_gather(const kvq_b8_cache &c, int batch, const int32_t *first,
+                             const int32_t *ends, int count, int bf16, void *k_out, void *v_out,
+                             cudaStream_t s);
+
+// The queries of an attention or mass call: sequence b's are rows cu_q[b] ..
+// cu_q[b + 1] - 1 (cu_q nullptr: row b).
+struct B8Queries {
+  const void *q;
+  int64_t token_stride, head_stride;  // elements
+  int bf16, num_heads, group;         // group = num_heads / kv heads
+  int batch, total_q, max_q;
+  const int32_t *cu_q, *seq_lens;
+  int max_seq_len;  // lengths are clamped to [0, max_seq_len]
+  float scale;
+};
+// How a call is cut: `row_tiles` tiles of `rows` (head, query) rows for each
+// (sequence, kv head), each over `splits` ranges of `split_tokens` tokens.
+struct B8Plan {
+  int rows, row_tiles, splits, split_tokens;
+};
+B8Plan plan_b8_attn(const kvq_b8_cache &c, int group, int batch, int max_q, int max_seq_len);
+size_t b8_attn_workspace_bytes(const kvq_b8_cache &c, int batch, const B8Plan &p);
+// out: q's dtype [total_q][num_heads][D]; lse: [total_q][num_heads] or nullptr
+cudaError_t launch_b8_attn(const kvq_b8_cache &c, const B8Queries &q, const B8Plan &p, void *out,
+                           float *lse, float *ws, cudaStream_t s);
+// mass: [batch][kv heads][mass_stride]
+cudaError_t launch_b8_mass(const kvq_b8_cache &c, const B8Queries &q, const float *lse,
+                           float *mass, int64_t mass_stride, cudaStream_t s);
+
+// kept: [batch][kv heads][keep], mass_out: [batch][kv heads][mass_out_stride]
+cudaError_t launch_b8_evict(const kvq_b8_cache &src, const kvq_b8_cache &dst, int batch,
+                            const int32_t *seq_lens, int max_seq_len, const float *mass,
+                            int64_t mass_stride, int keep, int recent, int sinks,
+                            int32_t *new_lens, int32_t *kept, float *mass_out,
+                            int64_t mass_out_stride, cudaStream_t s);
+
+}  // namespace kvq

@@ -1,0 +1,81 @@
+// rope.cu -- rotary positions on q and k (kvq_rope).
+//
+// a' = (a cos t - b sin t) f, b' = (b cos t + a sin t) f for each pair of the
+// leading rot_dim dims, t = position * inv_freq.  Bound: HBM, every element
+// read once and written once; the angles of a token are computed once for all
+// its heads and kept in shared memory.
+#include "rope.cuh"
+
+namespace kvq {
+namespace {
+
+using namespace rope;
+
+constexpr int kThreads = 256;
+constexpr int kTokens = 4;  // most tokens of one CTA
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads)
+    rope_kernel(kvq_rope_spec spec, int head_dim, int num_tokens, int tokens_per_cta,
+                const int32_t *__restrict__ positions, int inverse, kvq_heads q, kvq_heads q_out,
+                kvq_heads k, kvq_heads k_out) {
+  extern __shared__ float2 cs[];  // [tokens of the CTA][rot / 2]
+  const int t0 = blockIdx.x * tokens_per_cta;
+  const int nt = min(tokens_per_cta, num_tokens - t0);
+  const int pairs = spec.rot_dim / 2, pieces = head_dim / 16;
+  const float sign = inverse ? -1.f : 1.f;
+  for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
+    const int t = i / pairs, p = i - t * pairs;
+    float2 c = turn(__ldg(positions + t0 + t), __ldg(spec.d_inv_freq + p), spec.factor);
+    c.y *= sign;
+    cs[i] = c;
+  }
+  __syncthreads();
+  const int heads = q.num_heads + k.num_heads;
+  const int per_token = heads * pieces;
+  for (int i = threadIdx.x; i < nt * per_token; i += kThreads) {
+    const int t = i / per_token, r = i - t * per_token;
+    const int head = r / pieces, j = r - head * pieces;
+    const bool is_k = head >= q.num_heads;
+    const int h = is_k ? head - q.num_heads : head;
+    const kvq_heads &src = is_k ? k : q, &dst = is_k ? k_out : q_out;
+    const int64_t from = (int64_t)(t0 + t) * src.token_stride + h * src.head_stride;
+    const int64_t to = (int64_t)(t0 + t) * dst.token_stride + h * dst.head_stride;
+    const Piece p = piece(j, spec.rot_dim, spec.interleaved);
+    Raw8<BF16> a, b;
+    load8<BF16>(src.data, from + p.a, a);
+    load8<BF16>(src.data, from + p.b, b);
+    float u[8], v[8];
+    widen8<BF16>(a, u);
+    widen8<BF16>(b, v);
+    if (p.pair >= 0) {
+      float2 c[8];
+#pragma unroll
+      for (int e = 0; e < 8; e++) c[e] = cs[t * pairs + p.pair + e];
+      rotate_piece(u, v, c, spec.interleaved);
+    }
+    store8<BF16>(dst.data, to + p.a, u);
+    store8<BF16>(dst.data, to + p.b, v);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const kvq_rope_spec &spec, int bf16, int head_dim, int num_tokens,
+                        const int32_t *positions, int inverse, const kvq_heads &q,
+                        const kvq_heads &q_out, const kvq_heads &k, const kvq_heads &k_out,
+                        cudaStream_t s) {
+  if (num_tokens == 0) return cudaSuccess;
+  const int per = min(kTokens, max(1, num_tokens / (4 * kNumSMs)));
+  const int ctas = (num_tokens + per - 1) / per;
+  const size_t smem = (size_t)per * (spec.rot_dim / 2) * sizeof(float2);
+  if (bf16)
+    rope_kernel<true><<<ctas, kThreads, smem, s>>>(spec, head_dim, num_tokens, per, positions,
+                                                   inverse, q, q_out, k, k_out);
+  else
+    rope_kernel<false><<<ctas, kThreads, smem, s>>>(spec, head_dim, num_tokens, per, positions,
+                                                    inverse, q, q_out, k, k_out);
+  return cudaGetLastError();
+}
+
+}  // namespace kvq

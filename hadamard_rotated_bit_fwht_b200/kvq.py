@@ -33,6 +33,8 @@ EXPORTED = (
     "kvq_octave_codebook", "kvq_octave_quantize", "kvq_octave_decode_attn_workspace",
     "kvq_octave_decode_attn", "kvq_decode_attn_noalloc", "kvq_decode_step",
     "kvq_decode_attn_multi", "kvq_device_errors", "kvq_set_wait_limit",
+    "kvq_rope_frequencies", "kvq_rope", "kvq_b8_append", "kvq_b8_gather",
+    "kvq_b8_attn_workspace", "kvq_b8_attn", "kvq_b8_attn_mass", "kvq_b8_evict",
 )
 KVQ_DEVERR_WAIT_TIMEOUT, KVQ_DEVERR_BOUNDS = 1, 2
 
@@ -63,6 +65,34 @@ class OctaveFmtDesc(C.Structure):
 class OctaveLayoutDesc(C.Structure):
     _fields_ = [(n, C.c_int32) for n in ("off_k_nope", "off_v", "off_scales", "num_k_scales",
                                         "num_scales", "slot_bytes", "kernel_code")]
+
+
+class RopeDesc(C.Structure):
+    _fields_ = [("d_inv_freq", C.c_void_p), ("rot_dim", C.c_int32), ("interleaved", C.c_int32),
+                ("factor", C.c_float)]
+
+
+class HeadsDesc(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64),
+                ("num_heads", C.c_int32)]
+
+
+class B8CacheDesc(C.Structure):
+    _fields_ = [
+        ("k_codes", C.c_void_p), ("k_scales", C.c_void_p),
+        ("v_codes", C.c_void_p), ("v_scales", C.c_void_p),
+        ("num_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("block_size", C.c_int32),
+        ("num_blocks", C.c_int32), ("block_table", C.c_void_p), ("num_seqs", C.c_int32),
+        ("max_blocks_per_seq", C.c_int32),
+    ]
+
+
+class B8QueriesDesc(C.Structure):
+    _fields_ = [
+        ("q", HeadsDesc), ("dtype", C.c_int), ("batch", C.c_int32), ("total_q", C.c_int32),
+        ("max_q", C.c_int32), ("d_cu_q", C.c_void_p), ("d_seq_lens", C.c_void_p),
+        ("max_seq_len", C.c_int32), ("scale", C.c_float),
+    ]
 
 
 _lib = None
@@ -113,6 +143,28 @@ def lib():
                                       C.c_float, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]
         L.kvq_device_errors.argtypes = [C.POINTER(C.c_uint32)]
         L.kvq_set_wait_limit.argtypes = [C.c_int32]
+        L.kvq_rope_frequencies.argtypes = [C.c_int32, C.c_double, C.c_int, C.c_double, C.c_double,
+                                           C.c_double, C.c_double, C.c_void_p,
+                                           C.POINTER(C.c_float)]
+        L.kvq_rope.argtypes = [C.POINTER(RopeDesc), C.c_int, C.c_int32, C.c_int32, C.c_void_p,
+                               C.c_int32, C.POINTER(HeadsDesc), C.POINTER(HeadsDesc),
+                               C.POINTER(HeadsDesc), C.POINTER(HeadsDesc), C.c_void_p]
+        L.kvq_b8_append.argtypes = [C.POINTER(B8CacheDesc), C.POINTER(HeadsDesc),
+                                    C.POINTER(HeadsDesc), C.c_int, C.c_int32, C.c_int32,
+                                    C.c_void_p, C.c_void_p, C.POINTER(RopeDesc), C.c_void_p,
+                                    C.c_void_p]
+        L.kvq_b8_gather.argtypes = [C.POINTER(B8CacheDesc), C.c_int32, C.c_void_p, C.c_void_p,
+                                    C.c_int32, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p]
+        L.kvq_b8_attn_workspace.restype = C.c_size_t
+        L.kvq_b8_attn_workspace.argtypes = [C.POINTER(B8CacheDesc)] + [C.c_int32] * 4
+        L.kvq_b8_attn.argtypes = [C.POINTER(B8CacheDesc), C.POINTER(B8QueriesDesc), C.c_void_p,
+                                  C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]
+        L.kvq_b8_attn_mass.argtypes = [C.POINTER(B8CacheDesc), C.POINTER(B8QueriesDesc),
+                                       C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]
+        L.kvq_b8_evict.argtypes = [C.POINTER(B8CacheDesc), C.POINTER(B8CacheDesc), C.c_int32,
+                                   C.c_void_p, C.c_int32, C.c_void_p, C.c_int64, C.c_int32,
+                                   C.c_int32, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p,
+                                   C.c_int64, C.c_void_p]
         _lib = L
     return _lib
 
@@ -466,6 +518,342 @@ def octave_decode_attn(fmt: OctaveFormat, query: torch.Tensor, cache: torch.Tens
                sb.ctypes.data_as(C.c_void_p), _ptr(out), _ptr(workspace),
                workspace.numel() * workspace.element_size(), _stream(stream)))
     return out
+
+
+# --------------------------------------------------------------------------
+# Rotary positions
+# --------------------------------------------------------------------------
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def _here(**tensors):
+    """Refuse tensors that are not on the current CUDA device (the library
+    launches there); None entries are skipped."""
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be on the current CUDA device (cuda:{dev}), "
+                             f"got {t.device}")
+
+
+def _int32(name, t, numel):
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != numel:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {numel} values, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+
+
+def _empty(shape, dtype, like, stream):
+    """torch.empty that belongs to the stream the call runs on, so that its
+    memory is not handed out again while that stream still uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _heads(name, t):
+    """View of [..., heads, dim] as tokens x heads: the leading dims must step
+    through memory as one."""
+    if t.dim() < 3 or (t.stride(-1) != 1 and t.shape[-1] != 1):
+        raise ValueError(f"{name} must be [..., heads, dim] with dim contiguous")
+    step, span = 0, 1
+    for d in range(t.dim() - 3, -1, -1):
+        if t.shape[d] != 1:
+            if span == 1:
+                step = t.stride(d)
+            elif t.stride(d) != step * span:
+                raise ValueError(f"{name}: its tokens do not lie at one stride")
+            span *= t.shape[d]
+    # the stride of a dim of size 1 says nothing
+    head = t.stride(-2) if t.shape[-2] != 1 else 0
+    return HeadsDesc(t.data_ptr(), step, head, t.shape[-2])
+
+
+@dataclass(frozen=True)
+class Rope:
+    """A rotation of the leading 2 * len(inv_freq) dims of each head: radians
+    per position of every pair (fp64, on the device), whether pairs are
+    neighbouring dims or the two halves, and a factor on the rotated dims."""
+    inv_freq: torch.Tensor
+    interleaved: bool = False
+    factor: float = 1.0
+
+    @classmethod
+    def make(cls, rot_dim, base=10000.0, *, interleaved=False, scaling="none", scale=1.0,
+             trained_len=0, beta_fast=32.0, beta_slow=1.0, device="cuda"):
+        """The frequencies of kvq_rope_frequencies; scaling: "none", "linear",
+        "ntk" or "yarn"."""
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+        f = np.zeros(max(int(rot_dim) // 2, 1))
+        factor = C.c_float(1)
+        _check("kvq_rope_frequencies",
+               lib().kvq_rope_frequencies(int(rot_dim), float(base), ROPE_SCALINGS[scaling],
+                                          float(scale), float(trained_len), float(beta_fast),
+                                          float(beta_slow), f.ctypes.data_as(C.c_void_p),
+                                          C.byref(factor)))
+        return cls(torch.from_numpy(f).to(device), interleaved, float(factor.value))
+
+    def desc(self) -> RopeDesc:
+        f = self.inv_freq
+        if f.dtype != torch.float64 or f.dim() != 1 or not f.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous float64 vector")
+        return RopeDesc(f.data_ptr(), 2 * f.numel(), int(self.interleaved), self.factor)
+
+
+def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, rope: Rope, *,
+         inverse: bool = False, q_out: torch.Tensor | None = None,
+         k_out: torch.Tensor | None = None, stream=None):
+    """Rotate q and k ([..., heads, dim], any token and head stride) by their
+    tokens' positions (int32); returns (q_out, k_out).  q_out and k_out may be
+    q and k themselves.  inverse turns the other way (kvq_rope)."""
+    if q_out is None:
+        q_out = _empty(q.shape, q.dtype, q, stream)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+    elif k_out is None:
+        k_out = _empty(k.shape, k.dtype, k, stream)
+    _here(q=q, k=k, q_out=q_out, k_out=k_out, positions=positions, inv_freq=rope.inv_freq)
+    n = q.numel() // max(q.shape[-1] * q.shape[-2], 1)
+    _int32("positions", positions, n)
+    if q_out.shape != q.shape or q_out.dtype != q.dtype:
+        raise ValueError("q_out must have q's shape and dtype")
+    hk = hko = None
+    if k is not None:
+        if (k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1] or k.dtype != q.dtype
+                or k_out.shape != k.shape or k_out.dtype != k.dtype):
+            raise ValueError("k and k_out must match q's tokens, dim and dtype")
+        hk, hko = C.byref(_heads("k", k)), C.byref(_heads("k_out", k_out))
+    if n:
+        _check("kvq_rope",
+               lib().kvq_rope(C.byref(rope.desc()), _dtype_code(q), q.shape[-1], n,
+                              _ptr(positions), int(inverse), C.byref(_heads("q", q)),
+                              C.byref(_heads("q_out", q_out)), hk, hko, _stream(stream)))
+    return q_out, k_out
+
+
+# --------------------------------------------------------------------------
+# Block-scaled 8-bit cache
+# --------------------------------------------------------------------------
+class B8Cache:
+    """Paged int8 cache with one fp32 scale per (block of tokens, kv head):
+    planes [num_blocks, kv heads, block_size, dim] and [num_blocks, kv heads],
+    block table [num_seqs, columns] (layout in include/kvq.h)."""
+
+    def __init__(self, num_blocks, num_kv_heads, block_size, head_dim, block_table,
+                 device="cuda"):
+        codes = (num_blocks, num_kv_heads, block_size, head_dim)
+        dev = torch.device(device)
+        self._set(torch.zeros(codes, dtype=torch.int8, device=dev),
+                  torch.zeros(codes[:2], dtype=torch.float32, device=dev),
+                  torch.zeros(codes, dtype=torch.int8, device=dev),
+                  torch.zeros(codes[:2], dtype=torch.float32, device=dev), block_table)
+
+    @classmethod
+    def contiguous(cls, batch, num_kv_heads, max_tokens, head_dim, block_size=64, device="cuda"):
+        """Every sequence owns its blocks, in order."""
+        cols = (max_tokens + block_size - 1) // block_size
+        table = torch.arange(batch * cols, dtype=torch.int32, device=device).view(batch, cols)
+        return cls(batch * cols, num_kv_heads, block_size, head_dim, table, device)
+
+    @classmethod
+    def wrap(cls, k_codes, k_scales, v_codes, v_scales, block_table) -> "B8Cache":
+        """A cache over planes that the caller holds."""
+        c = cls.__new__(cls)
+        c._set(k_codes, k_scales, v_codes, v_scales, block_table)
+        return c
+
+    def with_block_table(self, block_table: torch.Tensor) -> "B8Cache":
+        """The same planes seen through another block table."""
+        return B8Cache.wrap(self.k_codes, self.k_scales, self.v_codes, self.v_scales, block_table)
+
+    def _set(self, k_codes, k_scales, v_codes, v_scales, block_table):
+        shape = k_codes.shape
+        if len(shape) != 4 or v_codes.shape != shape:
+            raise ValueError("codes must be [num_blocks, kv heads, block_size, dim]")
+        if k_scales.shape != shape[:2] or v_scales.shape != shape[:2]:
+            raise ValueError("scales must be [num_blocks, kv heads]")
+        for n, t, dt in (("k_codes", k_codes, torch.int8), ("v_codes", v_codes, torch.int8),
+                         ("k_scales", k_scales, torch.float32),
+                         ("v_scales", v_scales, torch.float32)):
+            if t.dtype != dt or t.device != k_codes.device or not t.is_contiguous():
+                raise ValueError(f"{n} must be a contiguous {dt} tensor on {k_codes.device}")
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [num_seqs, columns]")
+        bt = block_table.to(device=k_codes.device, dtype=torch.int32).contiguous()
+        self.k_codes, self.k_scales = k_codes, k_scales
+        self.v_codes, self.v_scales = v_codes, v_scales
+        self.block_table = bt
+        self.num_blocks, self.num_kv_heads, self.block_size, self.head_dim = shape
+        self._desc = B8CacheDesc(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                                 v_scales.data_ptr(), shape[1], shape[3], shape[2], shape[0],
+                                 bt.data_ptr(), bt.shape[0], bt.shape[1])
+
+    @property
+    def capacity(self):
+        return self.block_table.shape[1] * self.block_size
+
+    def desc(self) -> B8CacheDesc:
+        return self._desc
+
+
+def b8_append(cache: B8Cache, k: torch.Tensor, v: torch.Tensor, start_pos: torch.Tensor, *,
+              new_lens: torch.Tensor | None = None, rope: Rope | None = None,
+              positions: torch.Tensor | None = None, stream=None) -> None:
+    """Quantize k, v ([batch, t_new, Hkv, dim], any token and head stride) into
+    the cache at start_pos[b] + i, the first new_lens[b] tokens of each
+    sequence; rope rotates k first, by the storage positions or by `positions`
+    [batch, t_new] (kvq_b8_append)."""
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must have the same [batch, t_new, Hkv, dim] shape and dtype")
+    batch, t_new, hkv, dim = k.shape
+    if hkv != cache.num_kv_heads or dim != cache.head_dim:
+        raise ValueError("k and v do not match the cache's heads")
+    _here(cache=cache.k_codes, k=k, v=v, start_pos=start_pos, new_lens=new_lens,
+          positions=positions, inv_freq=None if rope is None else rope.inv_freq)
+    _int32("start_pos", start_pos, batch)
+    if new_lens is not None:
+        _int32("new_lens", new_lens, batch)
+    if positions is not None:
+        if rope is None:
+            raise ValueError("positions without rope")
+        _int32("positions", positions, batch * t_new)
+    if batch == 0 or t_new == 0:
+        return
+    _check("kvq_b8_append",
+           lib().kvq_b8_append(C.byref(cache.desc()), C.byref(_heads("k", k)),
+                               C.byref(_heads("v", v)), _dtype_code(k), batch, t_new,
+                               _ptr(start_pos), _ptr(new_lens),
+                               None if rope is None else C.byref(rope.desc()), _ptr(positions),
+                               _stream(stream)))
+
+
+def b8_gather(cache: B8Cache, first: torch.Tensor, ends: torch.Tensor, count: int,
+              dtype: torch.dtype = torch.bfloat16, k_out: torch.Tensor | None = None,
+              v_out: torch.Tensor | None = None, stream=None):
+    """Stored values of tokens first[b] .. first[b] + count - 1 as (k, v), each
+    [batch, count, Hkv, dim]; zeros from ends[b] on (kvq_b8_gather)."""
+    batch = first.numel()
+    shape = (batch, count, cache.num_kv_heads, cache.head_dim)
+    if k_out is None:
+        k_out = _empty(shape, dtype, cache.k_codes, stream)
+    if v_out is None:
+        v_out = _empty(shape, dtype, cache.k_codes, stream)
+    _here(cache=cache.k_codes, first=first, ends=ends, k_out=k_out, v_out=v_out)
+    _int32("first", first, batch)
+    _int32("ends", ends, batch)
+    for n, t in (("k_out", k_out), ("v_out", v_out)):
+        if t.shape != shape or t.dtype != k_out.dtype or not t.is_contiguous():
+            raise ValueError(f"{n} must be a contiguous {shape} tensor")
+    _check("kvq_b8_gather",
+           lib().kvq_b8_gather(C.byref(cache.desc()), batch, _ptr(first), _ptr(ends), int(count),
+                               _dtype_code(k_out), _ptr(k_out), _ptr(v_out), _stream(stream)))
+    return k_out, v_out
+
+
+def _b8_queries(cache, q, seq_lens, max_seq_len, scale, cu_q, max_q) -> B8QueriesDesc:
+    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.shape[1] % cache.num_kv_heads:
+        raise ValueError("q must be [queries, Hq, dim] with the cache's dim and Hq a multiple of "
+                         "its kv heads")
+    batch = seq_lens.numel()
+    _int32("seq_lens", seq_lens, batch)
+    if cu_q is None:
+        if q.shape[0] != batch:
+            raise ValueError("without cu_q there is one query per sequence")
+        max_q = 1
+    else:
+        _int32("cu_q", cu_q, batch + 1)
+        if max_q is None:
+            raise ValueError("cu_q needs max_q")
+    return B8QueriesDesc(_heads("q", q), _dtype_code(q), batch, q.shape[0], int(max_q),
+                         _ptr(cu_q), _ptr(seq_lens), int(max_seq_len), float(scale))
+
+
+def b8_attn_workspace(cache: B8Cache, batch: int, num_q_heads: int, max_seq_len: int,
+                      max_q: int = 1) -> int:
+    return int(lib().kvq_b8_attn_workspace(C.byref(cache.desc()), num_q_heads, batch, max_q,
+                                           max_seq_len))
+
+
+def b8_attn(cache: B8Cache, q: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
+            scale: float, *, cu_q: torch.Tensor | None = None, max_q: int | None = None,
+            return_lse: bool = False, out: torch.Tensor | None = None,
+            lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Attention of q [queries, Hq, dim] (any token and head stride) over the
+    cache: out [queries, Hq, dim] in q's dtype, and lse [queries, Hq] fp32 if
+    asked for.  One query per sequence, or sequence b's are rows cu_q[b] ..
+    cu_q[b + 1] - 1, at most max_q, under the causal rule (kvq_b8_attn)."""
+    d = _b8_queries(cache, q, seq_lens, max_seq_len, scale, cu_q, max_q)
+    if out is None:
+        out = _empty(q.shape, q.dtype, q, stream)
+    if lse is None and return_lse:
+        lse = _empty(q.shape[:2], torch.float32, q, stream)
+    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor of q's shape and dtype")
+    if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 [queries, Hq] tensor")
+    if workspace is None:
+        n = b8_attn_workspace(cache, d.batch, q.shape[1], d.max_seq_len, d.max_q)
+        if n:
+            workspace = _empty(n, torch.uint8, q, stream)
+    _here(cache=cache.k_codes, q=q, seq_lens=seq_lens, cu_q=cu_q, out=out, lse=lse,
+          workspace=workspace)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("kvq_b8_attn",
+           lib().kvq_b8_attn(C.byref(cache.desc()), C.byref(d), _ptr(out), _ptr(lse),
+                             _ptr(workspace), nbytes, _stream(stream)))
+    return (out, lse) if return_lse else out
+
+
+def b8_attn_mass(cache: B8Cache, q: torch.Tensor, lse: torch.Tensor, seq_lens: torch.Tensor,
+                 max_seq_len: int, scale: float, mass: torch.Tensor, *,
+                 cu_q: torch.Tensor | None = None, max_q: int | None = None,
+                 stream=None) -> None:
+    """Add to mass [batch, Hkv, >= max_seq_len] (fp32) the attention weight that
+    the queries of a b8_attn call, whose lse this is, give to each cached token
+    (kvq_b8_attn_mass)."""
+    d = _b8_queries(cache, q, seq_lens, max_seq_len, scale, cu_q, max_q)
+    if lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 [queries, Hq] tensor")
+    _b8_mass("mass", mass, cache, d.batch, d.max_seq_len)
+    _here(cache=cache.k_codes, q=q, lse=lse, seq_lens=seq_lens, cu_q=cu_q, mass=mass)
+    _check("kvq_b8_attn_mass",
+           lib().kvq_b8_attn_mass(C.byref(cache.desc()), C.byref(d), _ptr(lse), _ptr(mass),
+                                  mass.shape[2], _stream(stream)))
+
+
+def _b8_mass(name, t, cache, batch, tokens):
+    if (t.dim() != 3 or t.shape[0] != batch or t.shape[1] != cache.num_kv_heads
+            or t.shape[2] < tokens or t.dtype != torch.float32 or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous fp32 [{batch}, {cache.num_kv_heads}, "
+                         f">= {tokens}] tensor")
+
+
+def b8_evict(cache: B8Cache, into: B8Cache, mass: torch.Tensor, seq_lens: torch.Tensor,
+             max_seq_len: int, keep: int, *, recent: int = 0, sinks: int = 0,
+             mass_out: torch.Tensor | None = None, stream=None):
+    """Keep, for each sequence and kv head, the first `sinks`, the last `recent`
+    and the heaviest other tokens, `keep` in all, as tokens 0, 1, ... of
+    `into`, whose blocks must not be blocks of `cache`'s sequences.  Returns
+    (lengths [batch], kept old indices [batch, Hkv, keep], their mass [batch,
+    Hkv, keep] or mass_out) (kvq_b8_evict)."""
+    batch, hkv = seq_lens.numel(), cache.num_kv_heads
+    _int32("seq_lens", seq_lens, batch)
+    _b8_mass("mass", mass, cache, batch, int(max_seq_len))
+    lens = _empty(batch, torch.int32, mass, stream)
+    kept = _empty((batch, hkv, max(int(keep), 0)), torch.int32, mass, stream)
+    if mass_out is None:
+        mass_out = _empty(kept.shape, torch.float32, mass, stream)
+    _b8_mass("mass_out", mass_out, cache, batch, int(keep))
+    _here(cache=cache.k_codes, into=into.k_codes, mass=mass, seq_lens=seq_lens, mass_out=mass_out)
+    _check("kvq_b8_evict",
+           lib().kvq_b8_evict(C.byref(cache.desc()), C.byref(into.desc()), batch, _ptr(seq_lens),
+                              int(max_seq_len), _ptr(mass), mass.shape[2], int(keep), int(recent),
+                              int(sinks), _ptr(lens), _ptr(kept), _ptr(mass_out),
+                              mass_out.shape[2], _stream(stream)))
+    return lens, kept, mass_out
 
 
 # --------------------------------------------------------------------------

@@ -386,6 +386,208 @@ KVQ_API kvq_status kvq_octave_decode_attn(const kvq_octave_fmt *fmt, const void 
                                   float scale, const int32_t *sign_bits, float *out,
                                   void *workspace, size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------ */
+/* Rotary positions                                                           */
+/* ------------------------------------------------------------------------ */
+
+/* (The pages have no counterpart: rotary positions are what a model applies
+ * to q and k before they reach any of the caches here.)
+ * The rotation: pair i of the leading rot_dim dims of a head turns by
+ * t = position * inv_freq[i] radians,
+ *   a' = (a cos t - b sin t) * factor,   b' = (b cos t + a sin t) * factor,
+ * with (a, b) = dims (2i, 2i + 1) if interleaved, (i, i + rot_dim / 2)
+ * otherwise; dims from rot_dim on are copied.  Angles are formed in fp64 and
+ * reduced to one turn there, so far positions lose nothing; the rotation is
+ * fp32, rounded once to the output type. */
+typedef struct {
+  const double *d_inv_freq; /* device, rot_dim / 2 values, radians per position */
+  int32_t rot_dim;          /* a multiple of 16, at most head_dim */
+  int32_t interleaved;      /* 0: halves, 1: neighbouring dims form a pair */
+  float factor;             /* factor on the rotated dims (1 if none) */
+} kvq_rope_spec;
+
+/* Ways of stretching the frequencies beyond the trained context.  With
+ * f_i = base^(-2i / rot_dim):
+ *   KVQ_ROPE_NONE    f_i;
+ *   KVQ_ROPE_LINEAR  f_i / scale;
+ *   KVQ_ROPE_NTK     the frequencies of base * scale^(rot_dim / (rot_dim - 2));
+ *   KVQ_ROPE_YARN    f_i where pair i makes at least beta_fast turns within
+ *                    trained_len positions, f_i / scale where it makes at most
+ *                    beta_slow, a linear ramp in the number of turns between;
+ *                    the factor is 0.1 ln(scale) + 1. */
+typedef enum {
+  KVQ_ROPE_NONE = 0,
+  KVQ_ROPE_LINEAR = 1,
+  KVQ_ROPE_NTK = 2,
+  KVQ_ROPE_YARN = 3
+} kvq_rope_scaling;
+
+/* Host only: the frequencies above.  inv_freq: host, rot_dim / 2 doubles;
+ * factor: host.  rot_dim even and >= 2, base > 0, scale >= 1; for
+ * KVQ_ROPE_YARN trained_len > 0 and beta_fast > beta_slow. */
+KVQ_API kvq_status kvq_rope_frequencies(int32_t rot_dim, double base, kvq_rope_scaling kind,
+                                        double scale, double trained_len, double beta_fast,
+                                        double beta_slow, double *inv_freq, float *factor);
+
+/* Heads of a tensor [tokens][heads][head_dim]: element d of head h of token t
+ * is data[t * token_stride + h * head_stride + d] (strides in elements,
+ * multiples of 8; data 16-byte aligned), so q, k and v may be slices of one
+ * projection. */
+typedef struct {
+  void *data;
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t num_heads;
+} kvq_heads;
+
+/* kvq_rope -- rotate the heads of q and, if k is not NULL, of k.
+ *   d_positions: device int32[num_tokens], any value.
+ *   inverse: nonzero turns by -t: undoes the rotation (factor 1), and is its
+ *   transpose, so it maps the gradient of the outputs to that of the inputs.
+ *   q_out, k_out: as many heads as q and k; the same view as the input
+ *   (in place) or memory that does not overlap it.
+ * head_dim is a multiple of 16, at most 512 (KVQ_ERR_UNSUPPORTED otherwise,
+ * and for a rot_dim that is not a multiple of 16). */
+KVQ_API kvq_status kvq_rope(const kvq_rope_spec *spec, kvq_dtype dtype, int32_t head_dim,
+                            int32_t num_tokens, const int32_t *d_positions, int32_t inverse,
+                            const kvq_heads *q, const kvq_heads *q_out, const kvq_heads *k,
+                            const kvq_heads *k_out, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Block-scaled 8-bit cache                                                   */
+/* ------------------------------------------------------------------------ */
+
+/* (The pages have no counterpart.)  A paged cache of int8 codes with one fp32
+ * scale for each block of tokens and kv head: an element is code * scale.  No
+ * rotation is applied, so any head_dim of 64, 128 or 256 serves.
+ *   k_codes / v_codes   [num_blocks][num_kv_heads][block_size][head_dim] int8,
+ *                       16-byte aligned;
+ *   k_scales / v_scales [num_blocks][num_kv_heads] fp32; a block whose scale
+ *                       is 0 holds zero codes.
+ * Token t of sequence b lies in block block_table[b][t / block_size] at row
+ * t % block_size.  Table entries outside [0, num_blocks) are unmapped: appends
+ * skip them, reads give zeros and attention leaves their tokens out. */
+typedef struct {
+  int8_t *k_codes;
+  float *k_scales;
+  int8_t *v_codes;
+  float *v_scales;
+  int32_t num_kv_heads;       /* >= 1 */
+  int32_t head_dim;           /* 64, 128 or 256 */
+  int32_t block_size;         /* 16, 32, 64, 128 or 256 tokens */
+  int32_t num_blocks;         /* blocks in the planes */
+  const int32_t *block_table; /* device, [num_seqs][max_blocks_per_seq] */
+  int32_t num_seqs;
+  int32_t max_blocks_per_seq;
+} kvq_b8_cache;
+
+/* kvq_b8_append -- quantize new tokens of K and V into the cache.
+ *   k, v: views [batch * t_new tokens][num_kv_heads][head_dim] of `dtype`;
+ *   token i of sequence b is row b * t_new + i.
+ *   d_start_pos: device int32[batch]; token i goes to position
+ *   start_pos[b] + i; a token whose position is negative, past the table's
+ *   columns or on an unmapped block is skipped.
+ *   d_new_lens: device int32[batch] or NULL (t_new each): tokens i >=
+ *   new_lens[b] of a padded batch are neither read nor stored.
+ *   rope: NULL, or the rotation applied to k in fp32 before it is quantized;
+ *   d_rope_pos: device int32[batch * t_new] positions for it, or NULL for the
+ *   storage positions (they differ once tokens have been evicted).
+ * Per (block, kv head), with amax = max |x| over the block's new tokens (0 if
+ * below 2^-100) and `old` the block's scale if it holds tokens before
+ * start_pos[b], 0 otherwise: scale = max(amax / 127, old); codes are
+ * rint(x * (1 / scale)) in [-127, 127]; where the scale grew, the codes of the
+ * block's earlier tokens become rint(code * (old / scale)).  All in fp32,
+ * rounding to nearest even.  Rows behind the new tokens stay as they were.  A
+ * block must not be reached by two sequences of one call. */
+KVQ_API kvq_status kvq_b8_append(const kvq_b8_cache *cache, const kvq_heads *k,
+                                 const kvq_heads *v, kvq_dtype dtype, int32_t batch,
+                                 int32_t t_new, const int32_t *d_start_pos,
+                                 const int32_t *d_new_lens, const kvq_rope_spec *rope,
+                                 const int32_t *d_rope_pos, void *stream);
+
+/* kvq_b8_gather -- read stored values back: tokens first[b] .. first[b] +
+ * count - 1 of every sequence, as `dtype` (one rounding); tokens before 0, at
+ * or past ends[b], past the table or on an unmapped block give zeros.
+ *   k_out, v_out: device, [batch][count][num_kv_heads][head_dim], 16-byte
+ *   aligned.  d_first, d_ends: device int32[batch]. */
+KVQ_API kvq_status kvq_b8_gather(const kvq_b8_cache *cache, int32_t batch,
+                                 const int32_t *d_first, const int32_t *d_ends, int32_t count,
+                                 kvq_dtype dtype, void *k_out, void *v_out, void *stream);
+
+/* The queries of an attention or mass call: sequence b's are rows cu_q[b] ..
+ * cu_q[b + 1] - 1 of q, its last tokens; query i of n attends to the tokens
+ * t <= seq_lens[b] - n + i (none if that is negative).  Lengths are clamped to
+ * [0, min(max_seq_len, the table's tokens)].  A sequence whose query range
+ * leaves [0, total_q) or holds more than max_q has no queries; rows of no
+ * sequence are left as they were. */
+typedef struct {
+  kvq_heads q;               /* [total_q][num_q_heads][head_dim] of dtype;
+                                num_q_heads a multiple of num_kv_heads */
+  kvq_dtype dtype;
+  int32_t batch;
+  int32_t total_q;
+  int32_t max_q;             /* most queries of a sequence (read only with d_cu_q) */
+  const int32_t *d_cu_q;     /* device, batch + 1 values; NULL: one query per
+                                sequence, total_q == batch */
+  const int32_t *d_seq_lens; /* device, batch values: tokens in the cache */
+  int32_t max_seq_len;
+  float scale;               /* factor on q . k */
+} kvq_b8_queries;
+
+/* kvq_b8_attn -- attention over the cache: out = softmax(scale q K^T) V for
+ * each query and head (head j reads kv head j / (num_q_heads / num_kv_heads)).
+ *   out: device, [total_q][num_q_heads][head_dim] of q's dtype, 16-byte
+ *   aligned, not overlapping q; lse: NULL or device fp32 [total_q][num_q_heads],
+ *   the natural logarithm of the sum of exp(score).
+ *   workspace: device, 16-byte aligned, at least kvq_b8_attn_workspace bytes
+ *   (NULL if that is 0); calls that may run at the same time need one each.
+ * A query that attends to no token (or to unmapped blocks only) gives zeros
+ * and an lse of -inf.  Products are accurate to fp32 for KVQ_F32 queries (22
+ * bits of q and of the probabilities); for KVQ_BF16 q is exact and the
+ * probabilities are rounded to 11 bits before they meet V. */
+KVQ_API size_t kvq_b8_attn_workspace(const kvq_b8_cache *cache, int32_t num_q_heads,
+                                     int32_t batch, int32_t max_q, int32_t max_seq_len);
+KVQ_API kvq_status kvq_b8_attn(const kvq_b8_cache *cache, const kvq_b8_queries *queries,
+                               void *out, float *lse, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/* kvq_b8_attn_mass -- the attention weight that each cached token receives,
+ * added up: mass[b][h][t] += sum over the queries of sequence b that attend to
+ * t and the q heads of kv head h of exp(score - lse).
+ *   lse: device fp32 [total_q][num_q_heads] of kvq_b8_attn for the same
+ *   queries and cache (a query whose lse is -inf adds nothing);
+ *   mass: device fp32 [batch][num_kv_heads][mass_stride], mass_stride >=
+ *   max_seq_len; tokens at or past the length, or on unmapped blocks, are left
+ *   as they were. */
+KVQ_API kvq_status kvq_b8_attn_mass(const kvq_b8_cache *cache, const kvq_b8_queries *queries,
+                                    const float *lse, float *mass, int64_t mass_stride,
+                                    void *stream);
+
+/* kvq_b8_evict -- drop tokens by weight.  A (sequence, kv head) with n =
+ * seq_lens[b] > keep tokens keeps its first `sinks`, its last `recent` and,
+ * of the others, the keep - sinks - recent with the largest mass (equal
+ * masses: the lowest token; NaN counts as largest); one with n <= keep keeps
+ * all.  The kept tokens, in order, become tokens 0, 1, ... of sequence b of
+ * `dst`: their stored values are quantized again as a fresh append of K and V
+ * would (no rope).  Rows of a block behind the last kept token stay as they
+ * were.
+ *   src, dst: equal heads and dims; the same planes under another block table
+ *   or another cache.  Blocks of dst must be no blocks of src that the call
+ *   reads, and dst's table must hold keep tokens a sequence.
+ *   mass: device fp32 [batch][num_kv_heads][mass_stride].
+ *   new_lens: device int32[batch], min(n, keep);
+ *   kept: device int32[batch][num_kv_heads][keep], the kept tokens' old
+ *   indices, -1 behind the last;
+ *   mass_out: device fp32 [batch][num_kv_heads][mass_out_stride], not
+ *   overlapping mass, mass_out_stride >= keep: the kept tokens' mass, 0 behind
+ *   the last.
+ * recent + sinks <= keep, keep >= 1. */
+KVQ_API kvq_status kvq_b8_evict(const kvq_b8_cache *src, const kvq_b8_cache *dst, int32_t batch,
+                                const int32_t *d_seq_lens, int32_t max_seq_len,
+                                const float *mass, int64_t mass_stride, int32_t keep,
+                                int32_t recent, int32_t sinks, int32_t *new_lens, int32_t *kept,
+                                float *mass_out, int64_t mass_out_stride, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,570 @@
+"""GPU parity of rotary positions and of the block-scaled 8-bit cache (append,
+read back, attention, accumulated weight, eviction) against the plain forms of
+b8_reference.py.  Tolerances follow from the roundings that each call makes
+and are stated where they are used."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import b8_reference as ref
+from hadamard_rotated_bit_fwht_b200 import build, kvq
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    kvq.lib()
+    kvq.device_errors()
+    yield
+    assert kvq.device_errors() == 0
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def rand(seed, *shape, dtype=F32, outliers=False):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(shape, generator=g)
+    if outliers:
+        x[..., ::37] *= 16.0
+    return x.to(dtype).cuda()
+
+
+def filled(seed, lens, hkv, dim, block, spare=0, unmapped=()):
+    """A cache of random codes and scales over a shuffled table; (sequence,
+    column) pairs of `unmapped` have no block.  Blocks of no sequence hold NaN
+    scales."""
+    g = torch.Generator().manual_seed(seed)
+    cols = [(n + block - 1) // block for n in lens]
+    nb = sum(cols) + spare + 2
+    codes = [torch.randint(-127, 128, (nb, hkv, block, dim), generator=g, dtype=torch.int8)
+             for _ in "kv"]
+    scales = [torch.exp(torch.randn((nb, hkv), generator=g)) / 64 for _ in "kv"]
+    perm = torch.randperm(nb, generator=g).int()
+    table = torch.full((len(lens), max(cols + [1])), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(cols):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    for p in perm[at:].tolist():
+        for s in scales:
+            s[p] = math.nan
+    for b, col in unmapped:
+        table[b, col] = -1 if (b + col) % 2 else nb + 5
+    c = kvq.B8Cache.wrap(codes[0].cuda(), scales[0].cuda(), codes[1].cuda(), scales[1].cuda(),
+                         table.cuda())
+    return c, perm[at:]
+
+
+# ------------------------------------------------------------------ rope
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,hq,hkv,dim,rot,inter,fused", [
+    (1, 4, 1, 64, 64, False, False), (5, 8, 2, 128, 128, True, True),
+    (700, 3, 3, 128, 32, False, True), (2500, 4, 1, 256, 64, True, False),
+    (33, 1, 1, 16, 16, False, False), (3, 2, 1, 512, 512, True, False),
+    (7, 2, 2, 48, 16, False, True)])
+def test_rope(dtype, n, hq, hkv, dim, rot, inter, fused):
+    x = rand(n + dim, n, hq + 2 * hkv, dim, dtype=dtype)
+    q, k = x[:, :hq], x[:, hq:hq + hkv]
+    if not fused:
+        q, k = q.contiguous(), k.contiguous()
+    g = torch.Generator().manual_seed(n)
+    pos = torch.randint(0, 1 << 20, (n,), generator=g, dtype=torch.int32)
+    pos[0] = 0
+    pos[-1] = 2 ** 31 - 1
+    if n > 2:
+        pos[1] = -5
+    r = kvq.Rope.make(rot, interleaved=inter, scaling="yarn", scale=8.0, trained_len=4096)
+    for inverse in (False, True):
+        got = kvq.rope(q, k, pos.cuda(), r, inverse=inverse)
+        for a, b in zip(got, (q, k)):
+            want = ref.rotate(b, pos, r.inv_freq, r.factor, inter, inverse)
+            # fp32: the angle is off by 2^-25 half turns + its fp64 error (2^31
+            # radians keep 2^-21), sincospi by 2 ulp, the three products and
+            # sums by half an ulp each, all times |x| <= 6; then one rounding
+            tol = 6 * r.factor * 2 * (3.2 * 2 ** -25 + 2 ** -20 * (pos.double() / 2 ** 31).abs()
+                                      + 5 * 2 ** -24)[:, None, None]
+            tol = tol + want.abs() * torch.finfo(dtype).eps / 2
+            assert ((a.double().cpu() - want).abs() <= tol).all()
+            assert torch.equal(a[..., rot:], b[..., rot:])
+    # in place, and undone again: the same view as input and output
+    y = x.clone()
+    kvq.rope(y[:, :hq], y[:, hq:hq + hkv], pos.cuda(), r, q_out=y[:, :hq],
+             k_out=y[:, hq:hq + hkv])
+    fwd = kvq.rope(q, k, pos.cuda(), r)
+    assert torch.equal(y[:, :hq], fwd[0]) and torch.equal(y[:, hq:hq + hkv], fwd[1])
+    assert torch.equal(y[:, hq + hkv:], x[:, hq + hkv:])
+
+
+def test_rope_inverse_is_the_gradient():
+    """<rope(x), w> = <x, rope_inverse(w)>, and against central differences."""
+    n, h, d = 6, 2, 64
+    r = kvq.Rope.make(48, interleaved=True, scaling="yarn", scale=4.0, trained_len=2048)
+    x, w = rand(1, n, h, d), rand(2, n, h, d)
+    pos = ints([0, 1, 17, 999, 32768, 100000])
+    f = lambda x: (kvq.rope(x, None, pos, r)[0].double() * w.double()).sum().item()
+    grad = kvq.rope(w, None, pos, r, inverse=True)[0]
+    # the two sums have 768 terms below 30, each off by 2^-21 relative
+    assert abs(f(x) - (x.double() * grad.double()).sum().item()) < 768 * 30 * 2 ** -21
+    for i, j, e in ((0, 0, 3), (3, 1, 0), (5, 0, 47), (4, 1, 60)):
+        up, dn = x.clone(), x.clone()
+        up[i, j, e] += 1.0
+        dn[i, j, e] -= 1.0
+        # linear in x: the difference is exact but for the roundings of f's
+        # few changed terms (below 60, 2^-21 each)
+        assert abs((f(up) - f(dn)) / 2 - grad[i, j, e].item()) < 4 * 60 * 2 ** -21
+
+
+def test_rope_shapes_streams_and_empty():
+    r = kvq.Rope.make(64)
+    x = rand(3, 2, 5, 4, 64, dtype=BF16)
+    pos = ints(list(range(10)))
+    a, none = kvq.rope(x, None, pos, r)
+    assert none is None and a.shape == x.shape
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    b, _ = kvq.rope(x, None, pos, r, stream=st)
+    st.synchronize()
+    assert torch.equal(a, b)
+    e, _ = kvq.rope(x[:0], None, pos[:0], r)
+    assert e.shape == (0, 5, 4, 64)
+    with pytest.raises(ValueError):
+        kvq.rope(x, None, pos[:9], r)
+    with pytest.raises(ValueError):
+        kvq.rope(x, None, pos.long(), r)
+    with pytest.raises(TypeError):
+        kvq.rope(x.half(), None, pos, r)
+    with pytest.raises(ValueError):
+        kvq.rope(x.cpu(), None, pos, r)
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dim,block,hkv,start,new", [
+    (128, 16, 2, [5, 0, 31], [1, 1, 1]), (64, 32, 1, [0, 7, 64, 3], [40, 100, 0, 33]),
+    (256, 64, 3, [63, 10], [130, 2]), (128, 256, 1, [0, 255, 700], [256, 300, 1]),
+    (256, 256, 2, [17], [700]), (64, 128, 4, [-3, 120], [9, 9])])
+def test_append_and_gather(dtype, dim, block, hkv, start, new):
+    batch, t_new = len(start), max(new)
+    c, _ = filled(dim + block, [max(s + n, 1) for s, n in zip(start, new)], hkv, dim, block)
+    x = rand(7, batch, t_new, 3 * hkv, dim, dtype=dtype, outliers=True)
+    k, v = x[:, :, :hkv], x[:, :, hkv:2 * hkv]
+    x[0, 0, 0] = 0  # an empty row
+    before = ref.Cache(c)
+    kvq.b8_append(c, k, v, ints(start), new_lens=ints(new))
+    want = before
+    for b in range(batch):
+        want.append(b, start[b], k[b, :new[b]].float().cpu(), v[b, :new[b]].float().cpu())
+    # the fp32 operations are pinned: bit-exact, other rows untouched
+    for w, codes, scales in (("k", c.k_codes, c.k_scales), ("v", c.v_codes, c.v_scales)):
+        assert torch.equal(codes.cpu(), want.codes[w])
+        assert torch.equal(scales.cpu().view(torch.int32), want.scales[w].view(torch.int32))
+    ends = [max(s + n, 0) for s, n in zip(start, new)]
+    first = [max(e - 3, -1) for e in ends]
+    count = max(e - f for e, f in zip(ends, first)) + 2
+    for dt in (BF16, F32):
+        gk, gv = kvq.b8_gather(c, ints(first), ints(ends), count, dt)
+        for w, g in (("k", gk), ("v", gv)):
+            for b in range(batch):
+                val, _ = want.values(w, b, ends[b])
+                for i in range(count):
+                    t = first[b] + i
+                    row = val[:, t].float().to(dt) if 0 <= t < ends[b] else torch.zeros(hkv, dim)
+                    assert torch.equal(g[b, i].cpu().float(), row.float())
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("own_positions", [False, True])
+def test_append_with_rope(inter, own_positions):
+    batch, t_new, hkv, dim, block = 2, 70, 2, 128, 32
+    start, new = [10, 50], [70, 45]
+    r = kvq.Rope.make(64, interleaved=inter)
+    k, v = rand(11, batch, t_new, hkv, dim), rand(12, batch, t_new, hkv, dim)
+    c, _ = filled(13, [80, 95], hkv, dim, block)
+    c.k_scales.mul_(1e-3)
+    want = ref.Cache(c)
+    pos = torch.stack([torch.arange(t_new, dtype=torch.int32) * 3 + s for s in start])
+    if not own_positions:
+        pos = torch.stack([torch.arange(t_new, dtype=torch.int32) + s for s in start])
+    kvq.b8_append(c, k, v, ints(start), new_lens=ints(new), rope=r,
+                  positions=pos.cuda() if own_positions else None)
+    for b in range(batch):
+        kr = ref.rotate(k[b, :new[b]], pos[b, :new[b]], r.inv_freq, 1.0, inter).float()
+        want.append(b, start[b], kr, v[b, :new[b]].cpu())
+    # rotated values are off by 1e-6 (see test_rope; |x| <= 5), so scales by
+    # 1e-6 / 127 and codes by one where x / scale lies near a half
+    assert torch.equal(c.v_codes.cpu(), want.codes["v"])
+    ok = ~torch.isnan(want.scales["k"])
+    assert ((c.k_scales.cpu() - want.scales["k"]).abs()[ok] <= 1e-6 / 127 + 2 ** -23).all()
+    off = (c.k_codes.cpu().int() - want.codes["k"].int()).abs()
+    assert off.max() <= 1
+    assert (off > 0).float().mean() < 1e-3  # 127 * 1e-6 / (amax > 1) of a unit step, twice
+
+
+def test_append_skips_unmapped_blocks_and_tails():
+    c, _ = filled(21, [64, 64], 1, 64, 16, unmapped=[(0, 1), (1, 3)])
+    k, v = rand(22, 2, 64, 1, 64), rand(23, 2, 64, 1, 64)
+    want = ref.Cache(c)
+    kvq.b8_append(c, k, v, ints([0, 0]))
+    for b in range(2):
+        want.append(b, 0, k[b].cpu(), v[b].cpu())
+    assert torch.equal(c.k_codes.cpu(), want.codes["k"])
+    assert torch.equal(c.v_codes.cpu(), want.codes["v"])
+    # past the table's columns and at the far end of int32: nothing is stored
+    kvq.b8_append(c, k, v, ints([64, 2 ** 31 - 2]))
+    assert torch.equal(c.k_codes.cpu(), want.codes["k"])
+    gk, _ = kvq.b8_gather(c, ints([16, 2 ** 31 - 2]), ints([32, 2 ** 31 - 1]), 16, F32)
+    assert not gk.any()
+
+
+# ------------------------------------------------------------------ attention
+def tolerance(dtype, dim, tokens, a, want, vmax):
+    """Scores: q keeps 22 bits (bf16: all), each of the dim / 16 (twice that for
+    hi + lo) accumulations rounds or truncates at 2^-22 of at most a, the scaling
+    and the difference with the maximum at 2^-23 of it.  exp2 and the
+    probability's product: 2^-20.  Sums over tokens / 16 steps, a warp's share of
+    them, at 2^-23 each.  bf16: the probability is rounded to fp16 (2^-11), the
+    result to bf16."""
+    s = a * 2.0 ** -22 * (2 + dim / 16 * (1 if dtype == BF16 else 2)) + 2.0 ** -20
+    steps = tokens / 16 * 2.0 ** -23 + 16 * 2.0 ** -23
+    rel = 2 * s + steps + (2.0 ** -11 if dtype == BF16 else 0)
+    out = rel[..., None] * vmax
+    if dtype == BF16:
+        out = out + want.abs() * torch.finfo(BF16).eps / 2
+    return out, s + steps
+
+
+def check_attention(c, q, lens, cu, max_len, dtype, scale, **kw):
+    out, lse = kvq.b8_attn(c, q, ints(lens), max_len, scale,
+                           cu_q=None if cu is None else ints(cu),
+                           max_q=None if cu is None else max(np.diff(cu).max(), 1),
+                           return_lse=True, **kw)
+    r = ref.Cache(c)
+    at = list(range(len(lens) + 1)) if cu is None else cu
+    real = [min(max(n, 0), max_len) for n in lens]
+    want, wlse, a = ref.attention(r, q, real, at, scale)
+    scales = r.scales["v"][r.table[(r.table >= 0) & (r.table < r.nb)]]
+    vmax = 127 * (scales.nan_to_num(0).max().item() if scales.numel() else 0)
+    tol, ltol = tolerance(dtype, c.head_dim, max(real), a, want, vmax)
+    err = (out.double().cpu() - want).abs()
+    assert (err <= tol).all(), (err - tol).max()
+    fin = torch.isfinite(wlse)
+    got = lse.double().cpu()
+    assert torch.equal(fin, torch.isfinite(got)) and (got[~fin] == -math.inf).all()
+    assert ((got - wlse).abs()[fin] <= ltol[fin] + wlse.abs()[fin] * 2 ** -22).all()
+    return out, lse, r, real, at, a
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 3, 8, 16])
+def test_decode(dtype, dim, group):
+    lens = [0, 1, 15, 16, 17, 127, 128, 129, 300, 1000]
+    c, _ = filled(31 + dim, lens, 2, dim, 16 if group < 8 else 32,
+                  unmapped=[(8, 2), (9, 0), (9, 5)])
+    q = rand(32, len(lens), 2 * group, dim, dtype=dtype)
+    check_attention(c, q, lens, None, 1000, dtype, dim ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("block", [16, 64, 256])
+def test_decode_in_splits(dtype, block):
+    """Long enough for several ranges; lengths are clamped to max_seq_len, and a
+    sequence whose blocks are all unmapped attends to nothing."""
+    lens = [9001, 4096, 33, 500]
+    c, _ = filled(41, lens, 1, 128, block, unmapped=[(3, i) for i in range((500 - 1) // block + 1)])
+    q = rand(42, 4, 4, 128, dtype=dtype)
+    assert kvq.b8_attn_workspace(c, 4, 4, 9001) > 0
+    check_attention(c, q, lens, None, 9001, dtype, 0.05)
+    check_attention(c, q, [9001, 4096, -7, 500], None, 5000, dtype, 0.05)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dim,group,nq,lens", [
+    (64, 4, [1, 2, 3], [1, 100, 2]), (128, 1, [5, 0, 70], [70, 10, 70]),
+    (128, 5, [33, 17, 64], [33, 500, 40]), (128, 4, [130, 200], [1000, 200]),
+    (256, 8, [9, 40], [2000, 40]), (256, 2, [129, 65], [260, 64]), (128, 16, [3, 9], [300, 8]),
+    (64, 2, [300, 140], [700, 141])])
+def test_causal_prompts(dtype, dim, group, nq, lens):
+    """Ragged queries; more queries than tokens leave the first ones empty."""
+    c, _ = filled(51 + dim, lens, 2, dim, 32, unmapped=[(0, 1)] if lens[0] > 40 else [])
+    x = rand(52, sum(nq) + 3, 2 * group + 4, dim, dtype=dtype)
+    cu = [0] + np.cumsum(nq).tolist()
+    q = x[:sum(nq), 2:2 + 2 * group]
+    out, lse, r, real, at, a = check_attention(c, q, lens, cu, max(lens), dtype, dim ** -0.5)
+    # rows of no sequence stay as they were, in padded buffers too
+    big = torch.full((sum(nq) + 3, 2 * group, dim), 7.0, dtype=dtype, device="cuda")
+    blse = torch.full(big.shape[:2], 7.0, device="cuda")
+    kvq.b8_attn(c, x[:, 2:2 + 2 * group], ints(lens), max(lens), dim ** -0.5, cu_q=ints(cu),
+                max_q=max(nq), out=big, lse=blse)
+    assert torch.equal(big[:sum(nq)], out) and (big[sum(nq):] == 7).all()
+    assert torch.equal(blse[:sum(nq)], lse) and (blse[sum(nq):] == 7).all()
+    # the weights of the same queries
+    m0 = torch.rand((len(lens), 2, max(lens) + 5), generator=torch.Generator().manual_seed(1))
+    m = m0.cuda()
+    kvq.b8_attn_mass(c, q, lse, ints(lens), max(lens), dim ** -0.5, m, cu_q=ints(cu),
+                     max_q=max(nq))
+    check_mass(m, m0, r, q, lse, real, at, dim ** -0.5, a, dtype)
+
+
+def check_mass(m, m0, r, q, lse, real, at, scale, a, dtype):
+    want = ref.mass(r, q, lse, real, at, scale, m0)
+    # each weight: its score (see tolerance) and lse in log2 units (2^-22 of
+    # them), then sums over rows
+    fin = lse[torch.isfinite(lse)]
+    big = fin.abs().max().item() if fin.numel() else 0.0
+    dim = q.shape[2]
+    s = a.max().item() * 2.0 ** -22 * (2 + dim / 16 * 2) + 2.0 ** -20 + 2 * (big + 1) * 2.0 ** -22
+    rows = max(np.diff(at)) * q.shape[1]
+    tol = (want - m0.double()) * (2 * s + rows * 2.0 ** -24) + want.abs() * 2.0 ** -23
+    err = (m.double().cpu() - want).abs()
+    assert (err <= tol).all(), (err - tol).max()
+    for b, n in enumerate(real):  # behind the length: as it was
+        assert torch.equal(m[b, :, n:].cpu(), m0[b, :, n:])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dim,group", [(64, 1), (128, 4), (128, 16), (256, 5)])
+def test_mass_of_decode_steps(dtype, dim, group):
+    lens = [0, 1, 16, 31, 257, 5000]
+    c, _ = filled(61, lens, 2, dim, 16, unmapped=[(5, 3), (4, 0)])
+    q = rand(62, len(lens), 2 * group, dim, dtype=dtype)
+    out, lse, r, real, at, a = check_attention(c, q, lens, None, 5000, dtype, dim ** -0.5)
+    m0 = torch.rand((len(lens), 2, 5000), generator=torch.Generator().manual_seed(2))
+    m = m0.cuda()
+    kvq.b8_attn_mass(c, q, lse, ints(lens), 5000, dim ** -0.5, m)
+    check_mass(m, m0, r, q, lse, real, at, dim ** -0.5, a, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_wide_ranges_of_values(dtype):
+    """Block scales from 2^-60 to 2^60, zero scales, query rows from 2^-30 to
+    2^30, and scores of some hundreds: nothing overflows on the way."""
+    c, _ = filled(71, [400, 400], 1, 128, 16)
+    nb = c.num_blocks
+    e = torch.linspace(-60, 60, nb, device="cuda")[:, None]
+    c.v_scales.copy_(torch.exp2(e))
+    c.v_scales[3] = 0
+    c.v_codes[3] = 0
+    q = rand(72, 2, 4, 128)
+    q[0, 0] *= 2.0 ** -30
+    q[0, 1] *= 2.0 ** 9
+    q[1, 2] = 0
+    c.k_scales.nan_to_num_(1.0)
+    check_attention(c, q.to(dtype), [400, 390], None, 400, dtype, 0.1)
+    q[1, 3] *= 2.0 ** 30
+    c.k_scales.mul_(2.0 ** -30)
+    check_attention(c, q.to(dtype), [400, 390], None, 400, dtype, 0.1)
+
+
+def test_bad_query_ranges_have_no_queries():
+    c, _ = filled(81, [50, 50, 50], 1, 64, 16)
+    q = rand(82, 12, 2, 64)
+    out = torch.full_like(q, 5.0)
+    for cu in ([0, 4, 13, 13], [0, 4, 3, 3], [-1, -1, 12, 12], [0, 9, 12, 12]):
+        lse = torch.full((12, 2), 5.0, device="cuda")
+        kvq.b8_attn(c, q, ints([50] * 3), 50, 0.1, cu_q=ints(cu), max_q=8, out=out, lse=lse)
+        m = torch.zeros((3, 1, 50), device="cuda")
+        kvq.b8_attn_mass(c, q, torch.zeros((12, 2), device="cuda"), ints([50] * 3), 50, 0.1, m,
+                         cu_q=ints(cu), max_q=8)
+        for b in range(3):
+            n = cu[b + 1] - cu[b]
+            ok = cu[b] >= 0 and 0 < n <= 8 and cu[b + 1] <= 12
+            assert bool(m[b].any()) == ok
+            if ok:
+                assert not (out[cu[b]:cu[b + 1]] == 5).any()
+                out[cu[b]:cu[b + 1]] = 5.0
+        assert (out == 5).all()
+
+
+# ------------------------------------------------------------------ eviction
+@pytest.mark.parametrize("dim,block,to_block", [(64, 16, 16), (128, 32, 64), (256, 256, 256),
+                                                (128, 128, 16)])
+@pytest.mark.parametrize("keep,recent,sinks", [(1, 0, 0), (40, 8, 4), (64, 0, 0), (50, 30, 20),
+                                               (300, 100, 3)])
+def test_evict(dim, block, to_block, keep, recent, sinks):
+    lens = [0, 1, 39, 40, 41, 299, 301, 700]
+    c, _ = filled(91 + dim, lens, 2, dim, block, unmapped=[(7, 0)])
+    batch, n = len(lens), max(lens)
+    g = torch.Generator().manual_seed(keep)
+    m = torch.exp(2 * torch.randn((batch, 2, n + 3), generator=g))
+    m[:, 0] = (m[:, 0] * 2).round() / 2  # many ties, many zeros
+    m[7, 1, ::5] = 0.0
+    m[7, 1, 2::5] = -0.0
+    m[6, 1, 17] = math.inf
+    m[6, 1, 18] = math.nan
+    m[5, 1, 20] = -1.0
+    cols = (keep + to_block - 1) // to_block
+    into, _ = filled(92, [cols * to_block] * batch, 2, dim, to_block)
+    want, dst = ref.Cache(c), ref.Cache(into)
+    ln, kept, mo = kvq.b8_evict(c, into, m.cuda(), ints(lens), n, keep, recent=recent, sinks=sinks)
+    assert ln.tolist() == [min(x, keep) for x in lens]
+    for b in range(batch):
+        ids = want.evict(dst, b, lens[b], m[b], keep, recent, sinks)
+        for h in range(2):
+            k = len(ids[h])
+            assert kept[b, h, :k].tolist() == ids[h]
+            assert (kept[b, h, k:] == -1).all() and (mo[b, h, k:] == 0).all()
+            assert torch.equal(mo[b, h, :k].cpu().view(torch.int32),
+                               m[b, h, ids[h]].view(torch.int32))
+    # the fp32 operations are pinned: bit-exact, rows behind the last untouched
+    for w, codes, scales in (("k", into.k_codes, into.k_scales), ("v", into.v_codes, into.v_scales)):
+        assert torch.equal(codes.cpu(), dst.codes[w])
+        assert torch.equal(scales.cpu().view(torch.int32), dst.scales[w].view(torch.int32))
+
+
+def test_evict_long_and_equal_weights():
+    """More tokens than one pass of the threads, all weights equal: the lowest
+    indices stay."""
+    n, keep = 70000, 5000
+    table = torch.arange(n // 16 + 1 + (keep + 15) // 16, dtype=torch.int32)
+    c = kvq.B8Cache(table.numel(), 1, 16, 64, table[None, :n // 16 + 1].cuda())
+    into = c.with_block_table(table[None, n // 16 + 1:].cuda())
+    c.k_codes.random_(-127, 128)
+    c.k_scales.fill_(0.5)
+    m = torch.full((1, 1, n), 0.25, device="cuda")
+    _, kept, _ = kvq.b8_evict(c, into, m, ints([n]), n, keep, recent=100, sinks=7)
+    want = list(range(keep - 100)) + list(range(n - 100, n))
+    assert kept[0, 0].tolist() == want
+    wide = torch.empty((1, 1, keep + 50), device="cuda")
+    kvq.b8_evict(c, into, m, ints([n]), n, keep, mass_out=wide)
+    assert (wide[..., :keep] == 0.25).all() and (wide[..., keep:] == 0).all()
+
+
+# ------------------------------------------------------------------ as used
+def test_large_planes():
+    """Blocks beyond 2^32 bytes of a plane."""
+    bs, hkv, dim = 256, 8, 256
+    nb = (1 << 32) // (bs * hkv * dim) + 8
+    table = torch.tensor([[nb - 1, 2, nb - 3]], dtype=torch.int32)
+    c = kvq.B8Cache(nb, hkv, bs, dim, table.cuda())
+    k, v = rand(101, 1, 700, hkv, dim, dtype=BF16), rand(102, 1, 700, hkv, dim, dtype=BF16)
+    kvq.b8_append(c, k, v, ints([0]))
+    small = kvq.B8Cache(3, hkv, bs, dim, ints([[0, 1, 2]]))
+    kvq.b8_append(small, k, v, ints([0]))
+    q = rand(103, 40, 16, dim, dtype=BF16)
+    args = (q, ints([700]), 700, 1 / 16)
+    kw = dict(cu_q=ints([0, 40]), max_q=40, return_lse=True)
+    a, b = kvq.b8_attn(c, *args, **kw), kvq.b8_attn(small, *args, **kw)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ms = [torch.zeros((1, hkv, 700), device="cuda") for _ in "ab"]
+    for x, m in zip((c, small), ms):
+        kvq.b8_attn_mass(x, q, a[1], ints([700]), 700, 1 / 16, m, cu_q=ints([0, 40]), max_q=40)
+    assert torch.equal(*ms)
+    out = [kvq.b8_gather(x, ints([0]), ints([700]), 700) for x in (c, small)]
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    ev = [kvq.b8_evict(c, c.with_block_table(ints([[nb - 5]])), ms[0], ints([700]), 700, 200),
+          kvq.b8_evict(small, kvq.B8Cache(1, hkv, bs, dim, ints([[0]])), ms[1], ints([700]), 700,
+                       200)]
+    assert torch.equal(ev[0][1], ev[1][1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_serving_path(dtype):
+    """Prompt, decode steps that add up their weights, eviction, more steps with
+    true positions: the whole path against attention in fp64 over the values
+    the cache gives back."""
+    B, hq, hkv, dim, bs = 2, 8, 2, 128, 16
+    r = kvq.Rope.make(dim)
+    lens = [100, 61]
+    c = kvq.B8Cache(40, hkv, bs, dim, torch.randperm(40, generator=torch.Generator().manual_seed(3))
+                    .int().view(2, 20).cuda())
+    main, spare = c.with_block_table(c.block_table[:, :12]), c.with_block_table(
+        c.block_table[:, 12:])
+    k, v = rand(111, B, 100, hkv, dim, dtype=dtype), rand(112, B, 100, hkv, dim, dtype=dtype)
+    kvq.b8_append(main, k, v, ints([0, 0]), new_lens=ints(lens), rope=r)
+    m = torch.zeros((B, hkv, 192), device="cuda")
+    true_pos = list(lens)
+    cache = main
+    for step in range(12):
+        x = rand(120 + step, B, hq + 2 * hkv, dim, dtype=dtype)
+        q, kn, vn = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+        pos = ints(true_pos)
+        qr, _ = kvq.rope(q, None, pos, r)
+        kvq.b8_append(cache, kn[:, None], vn[:, None], ints(lens), rope=r, positions=pos[:, None])
+        lens = [n + 1 for n in lens]
+        true_pos = [n + 1 for n in true_pos]
+        out, lse, rc, real, at, a = check_attention(cache, qr, lens, None, 192, dtype, dim ** -0.5)
+        m0 = m.cpu()
+        kvq.b8_attn_mass(cache, qr, lse, ints(lens), 192, dim ** -0.5, m)
+        check_mass(m, m0, rc, qr, lse, real, at, dim ** -0.5, a, dtype)
+        if step == 7:
+            wide, before = torch.empty_like(m), m.cpu()
+            want, dst = ref.Cache(cache), ref.Cache(spare)
+            ln, kept, m = kvq.b8_evict(cache, spare, m, ints(lens), 192, 48, recent=16, sinks=4,
+                                       mass_out=wide)
+            for b in range(B):
+                ids = want.evict(dst, b, lens[b], before[b], 48, 16, 4)
+                assert kept[b].tolist() == ids
+            assert torch.equal(spare.k_codes.cpu(), dst.codes["k"])
+            assert torch.equal(spare.v_codes.cpu(), dst.codes["v"])
+            lens = ln.tolist()
+            assert lens == [48, 48]
+            cache = spare
+
+
+def test_streams_graphs_and_workspaces():
+    """Two graphs that share a workspace replay in turn, a call on another stream
+    with its own: the same results as an eager call; repeats are bit-identical."""
+    c, _ = filled(131, [6000, 3000], 2, 128, 32)
+    q = rand(132, 2, 8, 128, dtype=BF16)
+    lens = ints([6000, 3000])
+    want, wlse = kvq.b8_attn(c, q, lens, 6000, 0.08, return_lse=True)
+    m = torch.zeros((2, 2, 6000), device="cuda")
+    kvq.b8_attn_mass(c, q, wlse, lens, 6000, 0.08, m)
+    ws = torch.empty(kvq.b8_attn_workspace(c, 2, 8, 6000), dtype=torch.uint8, device="cuda")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    outs, graphs = [], []
+    with torch.cuda.stream(st):
+        for i in range(2):
+            out, lse = torch.empty_like(q), torch.empty_like(wlse)
+            mm = torch.zeros_like(m)
+            qi = q.clone() if i == 0 else (q * 0.5)
+            kvq.b8_attn(c, qi, lens, 6000, 0.08, out=out, lse=lse, workspace=ws)
+            st.synchronize()
+            gr = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(gr, stream=st):
+                kvq.b8_attn(c, qi, lens, 6000, 0.08, out=out, lse=lse, workspace=ws)
+                kvq.b8_attn_mass(c, qi, lse, lens, 6000, 0.08, mm)
+            outs.append((out, lse, mm, qi))
+            graphs.append(gr)
+        for o in outs:
+            o[0].zero_(), o[2].zero_()
+        for gr in (graphs[0], graphs[1], graphs[1], graphs[0]):
+            gr.replay()
+    st.synchronize()
+    assert torch.equal(outs[0][0], want) and torch.equal(outs[0][1], wlse)
+    assert torch.equal(outs[0][2], m + m)
+    half = kvq.b8_attn(c, outs[1][3], lens, 6000, 0.08)
+    assert torch.equal(outs[1][0], half)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        o = kvq.b8_attn(c, q, lens, 6000, 0.08, stream=other)
+        other.synchronize()
+        assert torch.equal(o, want)
+
+
+def test_refusals_on_the_device():
+    c, _ = filled(141, [64], 1, 64, 16)
+    q = rand(142, 1, 2, 64)
+    with pytest.raises(ValueError):
+        kvq.b8_attn(c, q, ints([64]).cpu(), 64, 0.1)
+    with pytest.raises(ValueError):
+        kvq.b8_attn(c, q, ints([64]), 64, 0.1, out=torch.empty_like(q).half())
+    with pytest.raises(TypeError):
+        kvq.b8_attn(c, q.half(), ints([64]), 64, 0.1)
+    with pytest.raises(kvq.KVQError) as e:
+        kvq.b8_attn(c, q, ints([64]), 64, float("nan"))
+    assert e.value.status == kvq.KVQ_ERR_INVALID_ARG
+    with pytest.raises(kvq.KVQError):
+        kvq.b8_evict(c, c, torch.zeros((1, 1, 64), device="cuda"), ints([64]), 64, 65)
+    e = kvq.b8_attn(c, q[:0], ints([]), 64, 0.1)
+    assert e.shape == (0, 2, 64)
