@@ -39,9 +39,10 @@ kvq_status check_b8(const kvq_b8_cache *c) {
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return KVQ_ERR_UNSUPPORTED;
   const int bs = c->block_size;
   if (bs != 16 && bs != 32 && bs != 64 && bs != 128 && bs != 256) return KVQ_ERR_UNSUPPORTED;
-  // grid rows, 32-bit row coordinates of the code planes and 32-bit positions
+  // grid rows, 32-bit row coordinates of the code planes and 32-bit positions (of tiles
+  // that end past the last token too)
   if (c->num_kv_heads > 65535 || (int64_t)c->num_blocks * c->num_kv_heads * bs >= (1LL << 31) ||
-      (int64_t)c->max_blocks_per_seq * bs >= (1LL << 31))
+      (int64_t)c->max_blocks_per_seq * bs >= (1LL << 31) - 4096)
     return KVQ_ERR_UNSUPPORTED;
   return KVQ_OK;
 }
@@ -176,15 +177,15 @@ kvq_status kvq_b8_gather(const kvq_b8_cache *cache, int32_t batch, const int32_t
                                     k_out, v_out, as_stream(stream)));
 }
 
-size_t kvq_b8_attn_workspace(const kvq_b8_cache *cache, int32_t num_q_heads, int32_t batch,
-                             int32_t max_q, int32_t max_seq_len) {
-  if (check_b8(cache) != KVQ_OK || num_q_heads < 1 || num_q_heads % cache->num_kv_heads ||
+size_t kvq_b8_attn_workspace(const kvq_b8_cache *cache, kvq_dtype dtype, int32_t num_q_heads,
+                             int32_t batch, int32_t max_q, int32_t max_seq_len) {
+  if (check_b8(cache) != KVQ_OK || !good_dtype(dtype) || num_q_heads < 1 || num_q_heads % cache->num_kv_heads ||
       batch < 1 || max_q < 1 || max_seq_len < 0)
     return 0;
   const int group = num_q_heads / cache->num_kv_heads;
-  if ((int64_t)max_q * group >= (1LL << 31) - 16) return 0;
+  if ((int64_t)max_q * group >= (1LL << 31) - 256) return 0;
   return b8_attn_workspace_bytes(*cache, batch,
-                                 plan_b8_attn(*cache, group, batch, max_q, max_seq_len));
+                                 plan_b8_attn(*cache, dtype == KVQ_BF16, group, batch, max_q, max_seq_len));
 }
 
 kvq_status kvq_b8_attn(const kvq_b8_cache *cache, const kvq_b8_queries *queries, void *out,
@@ -195,8 +196,8 @@ kvq_status kvq_b8_attn(const kvq_b8_cache *cache, const kvq_b8_queries *queries,
   if ((st = check_queries(*cache, queries, q)) != KVQ_OK) return st;
   if (q.batch == 0 || q.total_q == 0 || q.max_q == 0) return KVQ_OK;
   if (!out || !aligned(out, 16)) return KVQ_ERR_INVALID_ARG;
-  if ((int64_t)q.max_q * q.group >= (1LL << 31) - 16) return KVQ_ERR_UNSUPPORTED;
-  const B8Plan p = plan_b8_attn(*cache, q.group, q.batch, q.max_q, q.max_seq_len);
+  if ((int64_t)q.max_q * q.group >= (1LL << 31) - 256) return KVQ_ERR_UNSUPPORTED;
+  const B8Plan p = plan_b8_attn(*cache, q.bf16, q.group, q.batch, q.max_q, q.max_seq_len);
   if (!plan_fits(*cache, q.batch, p)) return KVQ_ERR_UNSUPPORTED;
   const size_t need = b8_attn_workspace_bytes(*cache, q.batch, p);
   if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))

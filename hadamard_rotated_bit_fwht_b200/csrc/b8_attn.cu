@@ -16,6 +16,7 @@
 //     products at most 2^14; l sums the unrounded p.
 #include <cuda_bf16.h>
 
+#include "b8_attn.cuh"
 #include "b8_mma.cuh"
 
 namespace kvq {
@@ -27,6 +28,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kEmpty = -1e30f;  // running maximum before any token
 constexpr float kSlack = 8.f;
+constexpr int64_t kPrefillRows = 64;
 
 template <int D, int R, bool HILO>
 struct Cfg {
@@ -46,15 +48,6 @@ struct Cfg {
   static constexpr int kOffM = kWarps * R * kRow * 4;
   static_assert(kOffM + kWarps * (2 * R + 1) * 4 <= kRing, "merge fits the ring");
   static_assert(kSmem * kCtas <= 227 * 1024, "shared memory per SM");
-};
-
-struct AttnArgs {
-  kvq_b8_cache c;
-  B8Queries q;
-  B8Plan p;
-  void *out;
-  float *lse, *ws;
-  uint32_t *err;
 };
 
 template <int D, bool HILO>
@@ -479,10 +472,14 @@ cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)a.q.batch * a.c.num_kv_heads * a.p.row_tiles;
   k<<<(unsigned)(units * a.p.splits), kThreads, C::kSmem, s>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || a.p.splits == 1) return e;
+  return cudaGetLastError();
+}
+
+template <int D, bool HILO>
+cudaError_t combine(const AttnArgs &a, cudaStream_t s) {
+  const int64_t units = (int64_t)a.q.batch * a.c.num_kv_heads * a.p.row_tiles;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * R));
+  cfg.gridDim = dim3((unsigned)(units * a.p.rows));
   cfg.blockDim = dim3(kCombine);
   cfg.stream = s;
   cudaLaunchAttribute at;
@@ -495,30 +492,45 @@ cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
 
 template <int D>
 cudaError_t by_rows(const AttnArgs &a, cudaStream_t s) {
-  if (a.p.rows == 8)
-    return a.q.bf16 ? launch<D, 8, false>(a, s) : launch<D, 8, true>(a, s);
-  return a.q.bf16 ? launch<D, 16, false>(a, s) : launch<D, 16, true>(a, s);
+  cudaError_t e;
+  if (a.p.prefill)
+    e = launch_b8_prefill(a, s);
+  else if (a.p.rows == 8)
+    e = a.q.bf16 ? launch<D, 8, false>(a, s) : launch<D, 8, true>(a, s);
+  else
+    e = a.q.bf16 ? launch<D, 16, false>(a, s) : launch<D, 16, true>(a, s);
+  if (e != cudaSuccess || a.p.splits == 1) return e;
+  return a.q.bf16 ? combine<D, false>(a, s) : combine<D, true>(a, s);
 }
+
+
 
 }  // namespace
 
-B8Plan plan_b8_attn(const kvq_b8_cache &c, int group, int batch, int max_q, int max_seq_len) {
+B8Plan plan_b8_attn(const kvq_b8_cache &c, int bf16, int group, int batch, int max_q,
+                    int max_seq_len) {
   B8Plan p;
   const int64_t rows = (int64_t)max_q * group;
-  p.rows = rows <= 8 ? 8 : 16;
-  p.row_tiles = (int)((rows + p.rows - 1) / p.rows);
-  const int64_t units = (int64_t)batch * c.num_kv_heads * p.row_tiles;
   const int64_t cap = (int64_t)c.max_blocks_per_seq * c.block_size;
   const int64_t len = max((int64_t)1, min((int64_t)max_seq_len, cap));
-  // about four CTAs for each that the card holds at once, of at least 16 tiles
-  // a warp where that leaves one CTA for each
-  const int resident = kNumSMs * (c.head_dim == 256 || p.rows == 16 ? 1 : 2);
-  const int64_t granule = kWarps * kTok;
-  const int64_t most = (len + granule - 1) / granule;
-  int64_t want = (4LL * resident + units - 1) / units;
-  const int64_t full = (resident + units - 1) / units;  // splits that fill the card once
-  want = min(want, max(full, (len + 2047) / 2048));
-  want = max((int64_t)1, min(want, most));
+  p.prefill = bf16 && rows >= kPrefillRows;
+  p.rows = p.prefill ? b8_prefill_rows(c.head_dim) : rows <= 8 ? 8 : 16;
+  p.row_tiles = (int)((rows + p.rows - 1) / p.rows);
+  const int64_t units = (int64_t)batch * c.num_kv_heads * p.row_tiles;
+  int64_t granule, want;
+  if (p.prefill) {
+    // one CTA per SM; two waves' worth where there are few units
+    granule = b8_prefill_tokens(c.head_dim);
+    want = min((int64_t)2 * kNumSMs / units, (len + 4 * granule - 1) / (4 * granule));
+  } else {
+    // about four CTAs for each that the card holds at once, of at least 16 tiles
+    // a warp where that leaves one CTA for each
+    const int resident = kNumSMs * (c.head_dim == 256 || p.rows == 16 ? 1 : 2);
+    const int64_t full = (resident + units - 1) / units;  // splits that fill the card once
+    granule = kWarps * kTok;
+    want = min((4 * (int64_t)resident + units - 1) / units, max(full, (len + 2047) / 2048));
+  }
+  want = max((int64_t)1, min(want, (len + granule - 1) / granule));
   int64_t tokens = (len + want - 1) / want;
   tokens = (tokens + granule - 1) / granule * granule;
   p.split_tokens = (int)tokens;
@@ -533,7 +545,7 @@ size_t b8_attn_workspace_bytes(const kvq_b8_cache &c, int batch, const B8Plan &p
 
 cudaError_t launch_b8_attn(const kvq_b8_cache &c, const B8Queries &q, const B8Plan &p, void *out,
                            float *lse, float *ws, cudaStream_t s) {
-  const AttnArgs a = {c, q, p, out, lse, ws, device_error_word()};
+  const AttnArgs a = {c, q, p, out, lse, ws, device_error_word(), wait_poll_limit()};
   switch (c.head_dim) {
     case 64: return by_rows<64>(a, s);
     case 128: return by_rows<128>(a, s);

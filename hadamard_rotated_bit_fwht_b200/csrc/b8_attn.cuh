@@ -1,0 +1,24 @@
+// b8_attn.cuh -- what the attention kernels of the block-scaled 8-bit cache
+// share.  Nothing here is part of the C ABI.
+#pragma once
+
+#include "b8_internal.cuh"
+
+namespace kvq {
+
+struct AttnArgs {
+  kvq_b8_cache c;
+  B8Queries q;
+  B8Plan p;
+  void *out;
+  float *lse, *ws;  // ws: records [unit][split][row of the tile] of m, l, -, -, O[D]
+  uint32_t *err;
+  int polls;  // limit of the bounded waits
+};
+
+// rows of a CTA and tokens of a tile of the many-row kernel
+int b8_prefill_rows(int head_dim);
+int b8_prefill_tokens(int head_dim);
+cudaError_t launch_b8_prefill(const AttnArgs &a, cudaStream_t s);
+
+}  // namespace kvq

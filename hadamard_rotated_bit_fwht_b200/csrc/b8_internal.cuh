@@ -35,8 +35,10 @@ struct B8Queries {
 // (sequence, kv head), each over `splits` ranges of `split_tokens` tokens.
 struct B8Plan {
   int rows, row_tiles, splits, split_tokens;
+  int prefill;  // 1: the many-row kernel
 };
-B8Plan plan_b8_attn(const kvq_b8_cache &c, int group, int batch, int max_q, int max_seq_len);
+B8Plan plan_b8_attn(const kvq_b8_cache &c, int bf16, int group, int batch, int max_q,
+                    int max_seq_len);
 size_t b8_attn_workspace_bytes(const kvq_b8_cache &c, int batch, const B8Plan &p);
 // out: q's dtype [total_q][num_heads][D]; lse: [total_q][num_heads] or nullptr
 cudaError_t launch_b8_attn(const kvq_b8_cache &c, const B8Queries &q, const B8Plan &p, void *out,

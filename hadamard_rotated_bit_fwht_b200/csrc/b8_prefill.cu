@@ -1,0 +1,589 @@
+// b8_prefill.cu -- many-row attention over the block-scaled 8-bit cache
+// (kvq_b8_attn with bf16 queries): both products on the fifth-generation
+// tensor cores, accumulators in tensor memory.
+//
+// A CTA takes kNT tiles of 128 rows (query, head of the group) of one
+// (sequence, kv head) and a range of tokens, kBN at a time.  Roles:
+//   softmax  one warpgroup per row tile, one row per thread: scores come from
+//            tensor memory, probabilities go back there as fp16 over them;
+//   convert  four warps: int8 codes from global memory to exact fp16 tiles in
+//            the 128-byte swizzle, K row by row (dims contiguous) and V in the
+//            same image, read by the second product with its dims as rows;
+//   issue    one thread: S(i) = Q K^T, O += P(i) V, two score buffers, so that
+//            one item's softmax runs beside the other's products.
+// Scores are scaled after the product: a row's factor is its thread's, a
+// block's scale one of 8 group constants of the tile.  The V scale joins the
+// exponent: p' = 2^(s - m + log2(64 v_scale / vref)), where vref is the
+// largest power-of-two bound of the V scales so far, so O is in units of vref / 64;
+// l sums p' of each 16-token group times the inverse of that factor.  The
+// maximum has a slack of 8, so O is rarely rescaled (by its softmax threads).
+// Bound: exp2 (16 a cycle and SM) and the tensor pipe alike.
+#include <cuda_bf16.h>
+
+#include "b8_attn.cuh"
+#include "b8_mma.cuh"
+
+namespace kvq {
+namespace {
+
+using namespace b8;
+using dec::mbar_arrive;
+using dec::mbar_init;
+
+template <int D>
+struct PCfg {
+  static constexpr int kNT = D == 256 ? 1 : 2;    // row tiles
+  static constexpr int kBN = D == 256 ? 64 : 128; // tokens of a tile
+  static constexpr int kGroups = kBN / 16;
+  static constexpr int kRows = 128 * kNT;
+  static constexpr int kSoft = 128 * kNT;
+  static constexpr int kThreads = kSoft + 128 + 32;
+  static constexpr int kQTileBytes = 128 * D * 2;
+  static constexpr int kKVBytes = kBN * D * 2;
+  static constexpr int kInfo = 4;                 // slots of group constants
+  static constexpr int kOffK = kNT * kQTileBytes;
+  static constexpr int kOffV = kOffK + 2 * kKVBytes;
+  static constexpr int kOffInfo = kOffV + 2 * kKVBytes;
+  static constexpr int kInfoFloats = 3 * 8 + 4;   // k factor, log2 v factor, its inverse; vref
+  static constexpr int kOffBar = kOffInfo + kInfo * kInfoFloats * 4;
+  // k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2],
+  // o_done[2], info_full[4], drain
+  static constexpr int kBars = 19;
+  static constexpr int kOffMisc = kOffBar + kBars * 8;  // abort flag, tensor memory base
+  static constexpr int kUsed = kOffMisc + 16 + 1024;    // 1024: alignment
+  // one CTA per SM (it takes all of tensor memory)
+  static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
+  static constexpr int kColO = 0, kColS = kNT * D;
+  static_assert(kColS + 2 * kBN <= 512, "tensor memory columns");
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
+
+// ---- tcgen05
+__device__ __forceinline__ void t5_alloc(uint32_t dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
+               "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void t5_dealloc(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+               : "memory");
+}
+__device__ __forceinline__ void t5_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void t5_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void t5_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void t5_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void t5_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+// 32 columns of this thread's lane
+__device__ __forceinline__ void t5_ld32(uint32_t addr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+      "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+#pragma unroll
+  for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void t5_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void t5_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void t5_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle.  K-major operands: rows
+// of 64 halves, groups of 8 rows `stride` bytes apart.  MN-major ones: 64
+// halves of the M or N extent per 128-byte row, groups of 8 k rows `stride`
+// bytes apart, further 64 of M or N `lead` bytes away.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lead >> 4) << 16 |
+         (uint64_t)(stride >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// fp16 operands, fp32 accumulator, M = 128
+__device__ __forceinline__ constexpr uint32_t instr_desc(int n, bool b_mn_major) {
+  return 1u << 4 | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
+}
+
+// 16 codes -> 16 exact halves
+__device__ __forceinline__ void widen16(const uint4 &w, uint4 (&h)[2]) {
+  k_frag(w.x, h[0].x, h[0].y);
+  k_frag(w.y, h[0].z, h[0].w);
+  k_frag(w.z, h[1].x, h[1].y);
+  k_frag(w.w, h[1].z, h[1].w);
+}
+
+template <int D>
+__global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
+    b8_prefill_kernel(const __grid_constant__ AttnArgs a) {
+  using C = PCfg<D>;
+  constexpr int kBN = C::kBN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const kvq_b8_cache &c = a.c;
+
+  // split fastest, then (kv head, sequence); row tiles from the last, whose
+  // token ranges are the longest, to the first
+  int u = blockIdx.x;
+  const int split = u % a.p.splits;
+  u /= a.p.splits;
+  const int bh = u % (a.q.batch * c.num_kv_heads);
+  const int rt = a.p.row_tiles - 1 - u / (a.q.batch * c.num_kv_heads);
+  const int kvh = bh % c.num_kv_heads, b = bh / c.num_kv_heads;
+  int q0;
+  const int nq = query_range(a.q, b, q0);
+  const int n_rows = nq * a.q.group, row0 = rt * C::kRows;
+  if (row0 >= n_rows) return;
+  const int len = seq_len(a.q, c, b);
+  const int i_last = (min(row0 + C::kRows, n_rows) - 1) / a.q.group;
+  const int hi_lim = max(0, len - nq + i_last + 1);
+  const int t0 = split * a.p.split_tokens;  // a multiple of kBN
+  const int t1 = min(hi_lim, t0 + a.p.split_tokens);
+  if (t0 >= t1 && split > 0) return;
+  const int nt = C::kNT == 2 && n_rows - row0 > 128 ? 2 : 1;
+  const int n_tiles = t1 > t0 ? (t1 - t0 + kBN - 1) / kBN : 0;
+  const int n_items = n_tiles * nt;
+
+  const uint32_t base = smem_u32(smem);
+  const uint32_t bars = base + C::kOffBar;
+  const uint32_t k_full = bars, k_empty = bars + 16, v_full = bars + 32, v_empty = bars + 48,
+                 s_full = bars + 64, p_full = bars + 80, o_done = bars + 96, info_full = bars + 112,
+                 drain = bars + 144;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc);
+  uint32_t *tmem_at = reinterpret_cast<uint32_t *>(smem + C::kOffMisc + 4);
+  float *info = reinterpret_cast<float *>(smem + C::kOffInfo);
+  constexpr int kIssueWarp = C::kThreads / 32 - 1;
+  if (tid == 0) {
+    for (int i = 0; i < 2; i++) {
+      mbar_init(k_full + 8 * i, 128);
+      mbar_init(k_empty + 8 * i, 1);
+      mbar_init(v_full + 8 * i, 128);
+      mbar_init(v_empty + 8 * i, 1);
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_full + 8 * i, 128);
+      mbar_init(o_done + 8 * i, 1);
+    }
+    for (int i = 0; i < C::kInfo; i++) mbar_init(info_full + 8 * i, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kIssueWarp) t5_alloc(base + C::kOffMisc + 4, 512);
+
+  // bounded wait; false once any thread of the CTA has given up
+  auto wait1 = [&](uint32_t bar, uint32_t parity) {
+    if (dec::mbar_wait(bar, parity, abort_flag, a.polls)) return true;
+    *abort_flag = 1;
+    dec::report(a.err, KVQ_DEVERR_WAIT_TIMEOUT);
+    return false;
+  };
+  // the same for a whole warp: one answer for all lanes
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait1(bar, parity)) != 0;
+  };
+
+  // ---- queries: a thread brings its row into [2^13, 2^14) by a power of two
+  // and stores it as fp16
+  const int wg = warp >> 2;  // row tile of a softmax warp
+  const int r = tid & 127;
+  const int row = row0 + wg * 128 + r;
+  const bool soft = tid < C::kSoft && wg < nt;
+  const bool live = soft && row < n_rows;
+  const int qi = live ? row / a.q.group : 0;
+  const int head = kvh * a.q.group + (live ? row - qi * a.q.group : 0);
+  float inv = 0.f;
+  if (soft) {
+    const uint4 *src = reinterpret_cast<const uint4 *>(
+        static_cast<const uint16_t *>(a.q.q) + (int64_t)(q0 + qi) * a.q.token_stride +
+        (int64_t)head * a.q.head_stride);
+    float m = 0.f;
+#pragma unroll 8
+    for (int ch = 0; ch < D / 8; ch++) {
+      const uint4 w = live ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        m = fmax_nan(m, fmax_nan(fabsf(bf16lo(ww[e])), fabsf(bf16hi(ww[e]))));
+    }
+    // the sign of the scale goes into q, so that scores grow with products
+    const float f = copysignf(query_scale(m), a.q.scale);
+    inv = __fdiv_rn(a.q.scale * kLog2e, f);
+    uint8_t *dst = smem + wg * C::kQTileBytes + r * 128;
+#pragma unroll 8
+    for (int ch = 0; ch < D / 8; ch++) {
+      const uint4 w = live ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
+      uint4 h;
+      h.x = pack_f16x2(bf16lo(w.x) * f, bf16hi(w.x) * f);
+      h.y = pack_f16x2(bf16lo(w.y) * f, bf16hi(w.y) * f);
+      h.z = pack_f16x2(bf16lo(w.z) * f, bf16hi(w.z) * f);
+      h.w = pack_f16x2(bf16lo(w.w) * f, bf16hi(w.w) * f);
+      *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (128 * 128) + (((ch & 7) ^ (r & 7)) << 4)) = h;
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  t5_before();
+  __syncthreads();
+  t5_after();
+  const uint32_t tmem = *tmem_at;
+
+  if (soft) {
+    // ---------------------------------------------------------- softmax
+    const int lim = live ? max(0, len - nq + qi + 1) : 0;
+    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // 32 lanes a warp
+    const uint32_t o_at = lanes + C::kColO + wg * D;
+    float m = -1e30f, l = 0.f, vref = 0x1p-100f;
+    bool ok = true;
+    for (int j = 0; j < n_tiles; j++) {
+      const int i = j * nt + wg, buf = i & 1;
+      const uint32_t s_at = lanes + C::kColS + buf * kBN;
+      if (!wait(info_full + 8 * (j & 3), (j >> 2) & 1) || !wait(s_full + 8 * buf, (i >> 1) & 1)) {
+        ok = false;
+        break;
+      }
+      t5_after();
+      const float *in = info + (j & 3) * C::kInfoFloats;
+      const int tok = t0 + j * kBN;
+      const bool cut = __any_sync(0xffffffffu, tok + kBN > lim);
+      // row maximum
+      float mx = -INFINITY;
+#pragma unroll
+      for (int ch = 0; ch < kBN / 32; ch++) {
+        float s[32];
+        t5_ld32(s_at + 32 * ch, s);
+        t5_wait_ld();
+#pragma unroll
+        for (int gr = 0; gr < 2; gr++) {
+          const float f = inv * in[2 * ch + gr];
+          // unmapped groups have a log2 factor of -inf
+          const float bias = in[8 + 2 * ch + gr] == -INFINITY ? -INFINITY : 0.f;
+          if (cut) {
+            const int left = lim - (tok + 32 * ch + 16 * gr);
+#pragma unroll
+            for (int e = 0; e < 16; e++)
+              mx = fmaxf(mx, e < left ? fmaf(s[16 * gr + e], f, bias) : -INFINITY);
+          } else {
+            float g0 = s[16 * gr], g1 = s[16 * gr + 1];
+#pragma unroll
+            for (int e = 2; e < 16; e += 2) {
+              g0 = fmaxf(g0, s[16 * gr + e]);
+              g1 = fmaxf(g1, s[16 * gr + e + 1]);
+            }
+            mx = fmaxf(mx, fmaf(fmaxf(g0, g1), f, bias));
+          }
+        }
+      }
+      const float nref = in[24];
+      const bool grow = mx > m + 8.f;
+      if (__any_sync(0xffffffffu, grow) || nref != vref) {
+        const float mn = grow ? mx : m;
+        const float al = ex2(m - mn);
+        l *= al;
+        m = mn;
+        if (j > 0) {
+          const float f = al * __fdiv_rn(vref, nref);
+          if (!wait(o_done + 8 * wg, (j - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          t5_after();
+#pragma unroll 1
+          for (int ch = 0; ch < D / 32; ch++) {
+            float o[32];
+            t5_ld32(o_at + 32 * ch, o);
+            t5_wait_ld();
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; e++) w[e] = __float_as_uint(o[16 * h + e] * f);
+              t5_st16(o_at + 32 * ch + 16 * h, w);
+            }
+          }
+        }
+        vref = nref;
+      }
+      // probabilities, over the scores that were read
+#pragma unroll
+      for (int ch = 0; ch < kBN / 32; ch++) {
+        float s[32];
+        t5_ld32(s_at + 32 * ch, s);
+        t5_wait_ld();
+        uint32_t w[16];
+#pragma unroll
+        for (int gr = 0; gr < 2; gr++) {
+          const float f = inv * in[2 * ch + gr], cst = in[8 + 2 * ch + gr] - m;
+          const int left = cut ? lim - (tok + 32 * ch + 16 * gr) : 16;
+          float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            float p0 = ex2(fmaf(s[16 * gr + e], f, cst));
+            float p1 = ex2(fmaf(s[16 * gr + e + 1], f, cst));
+            if (cut) {
+              p0 = e < left ? p0 : 0.f;
+              p1 = e + 1 < left ? p1 : 0.f;
+            }
+            sum0 += p0;
+            sum1 += p1;
+            w[8 * gr + e / 2] = pack_f16x2(p0, p1);
+          }
+          l = fmaf(sum0 + sum1, in[16 + 2 * ch + gr], l);
+        }
+        t5_st16(s_at + 16 * ch, w);
+      }
+      t5_wait_st();
+      t5_before();
+      mbar_arrive(p_full + 8 * buf);
+    }
+    // ---- result
+    if (ok && n_tiles > 0) ok = wait(o_done + 8 * wg, (n_tiles - 1) & 1);
+    t5_after();
+    const bool direct = a.p.splits == 1;
+    const float nan = __int_as_float(0x7fc00000);
+    float norm = vref * 0x1p-6f;
+    if (direct) norm = l > 0.f ? norm / l : l == 0.f ? 0.f : l;
+    if (!ok) norm = m = l = nan;
+    const int64_t orow = (int64_t)(q0 + qi) * a.q.num_heads + head;
+    const int64_t unit = (int64_t)bh * a.p.row_tiles + rt;
+    float *rec = a.ws + ((unit * a.p.splits + split) * C::kRows + wg * 128 + r) * (D + 4);
+#pragma unroll 1
+    for (int ch = 0; ch < D / 32; ch++) {
+      float o[32];
+      __syncwarp();
+      if (n_tiles > 0) {
+        t5_ld32(o_at + 32 * ch, o);
+        t5_wait_ld();
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; e++) o[e] = 0.f;
+      }
+      if (!live) continue;
+#pragma unroll
+      for (int e = 0; e < 32; e++) o[e] = norm == 0.f ? 0.f : o[e] * norm;
+      if (direct) {
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + orow * D + 32 * ch);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          uint4 w;
+          uint32_t *x = &w.x;
+#pragma unroll
+          for (int h = 0; h < 4; h++) {
+            const __nv_bfloat162 y = __floats2bfloat162_rn(o[8 * e + 2 * h], o[8 * e + 2 * h + 1]);
+            x[h] = *reinterpret_cast<const uint32_t *>(&y);
+          }
+          dst[e] = w;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+          *reinterpret_cast<float4 *>(rec + 4 + 32 * ch + 4 * e) =
+              make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+      }
+    }
+    if (live) {
+      if (!direct)
+        rec[0] = m, rec[1] = l;
+      else if (a.lse != nullptr)
+        a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+    }
+  } else if (tid >= C::kSoft && warp < kIssueWarp) {
+    // ---------------------------------------------------------- convert
+    constexpr int kPer = kBN * D / 16 / 128;  // 16-code pieces a thread has of a tile
+    const int ct = tid - C::kSoft;
+    const int32_t *table = c.block_table + (int64_t)b * c.max_blocks_per_seq;
+    // lane l: block of 16-token group l % kGroups of tile j, -1 if unmapped or
+    // past the range
+    auto slots_of = [&](int j) {
+      const int t = t0 + j * kBN + (lane % C::kGroups) * 16;
+      int p = -1;
+      if (j < n_tiles && t < t1) {
+        p = __ldg(table + t / c.block_size);
+        if (p < 0 || p >= c.num_blocks || !in_bounds(p, p + 1, c.num_blocks, a.err)) p = -1;
+      }
+      return p;
+    };
+    // piece i of this thread: plane (64 dims) pl, token tr, 16 dims 16 cc
+    auto load = [&](const int8_t *codes, int j, int slots, uint4 (&x)[kPer]) {
+#pragma unroll
+      for (int i = 0; i < kPer; i++) {
+        const int p = ct + 128 * i, pl = p / (4 * kBN), tr = (p >> 2) % kBN, cc = p & 3;
+        const int slot = __shfl_sync(0xffffffffu, slots, tr >> 4);
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (slot >= 0) {
+          const int at = (t0 + j * kBN + tr) % c.block_size;
+          x[i] = ldg_stream_u4(codes + (((int64_t)slot * c.num_kv_heads + kvh) * c.block_size + at) * D +
+                               64 * pl + 16 * cc);
+        }
+      }
+    };
+    auto put = [&](uint8_t *dst, const uint4 (&x)[kPer]) {
+#pragma unroll
+      for (int i = 0; i < kPer; i++) {
+        const int p = ct + 128 * i, pl = p / (4 * kBN), tr = (p >> 2) % kBN, cc = p & 3;
+        uint4 h[2];
+        widen16(x[i], h);
+        uint8_t *at = dst + pl * (kBN * 128) + tr * 128;
+        *reinterpret_cast<uint4 *>(at + (((2 * cc) ^ (tr & 7)) << 4)) = h[0];
+        *reinterpret_cast<uint4 *>(at + (((2 * cc + 1) ^ (tr & 7)) << 4)) = h[1];
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    };
+    float vref = 0x1p-100f;
+    int slots = slots_of(0);
+    uint4 kx[kPer], vx[kPer];
+    if (n_tiles > 0) load(c.k_codes, 0, slots, kx);
+    for (int j = 0; j < n_tiles; j++) {
+      const int st = j & 1;
+      load(c.v_codes, j, slots, vx);
+      float ks = 0.f, vs = 0.f;
+      if (warp == C::kSoft / 32 && slots >= 0) {
+        ks = __ldg(c.k_scales + (int64_t)slots * c.num_kv_heads + kvh);
+        vs = __ldg(c.v_scales + (int64_t)slots * c.num_kv_heads + kvh);
+      }
+      if (j >= 2 && !wait(k_empty + 8 * st, ((j - 2) >> 1) & 1)) break;
+      put(smem + C::kOffK + st * C::kKVBytes, kx);
+      mbar_arrive(k_full + 8 * st);
+      if (warp == C::kSoft / 32) {
+        // the tile's group constants; slot j % 4 was last read for tile j - 4,
+        // whose second product was waited for before V of tile j - 2 was stored
+        float vm = vs;
+#pragma unroll
+        for (int o = 1; o < C::kGroups; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+        if (vm > vref) vref = __uint_as_float((__float_as_uint(vm) + 0x7fffffu) & 0x7f800000u);
+        // blocks of scale 0 hold zeros: any factor serves.  Below 2^-40 of
+        // vref nothing reaches fp16's range: the factor stops at 2^-46, so
+        // that l keeps its terms
+        const float ratio = vs == 0.f ? 1.f : __fdiv_rn(vs, vref);
+        float lv = fmaxf(log2f(ratio), -46.f) + 6.f;
+        if (ratio != ratio) lv = ratio;
+        float *in = info + (j & 3) * C::kInfoFloats;
+        if (lane < C::kGroups) {
+          in[lane] = ks;
+          in[8 + lane] = slots >= 0 ? lv : -INFINITY;
+          in[16 + lane] = slots >= 0 ? ex2(-lv) : 0.f;
+          if (lane == 0) in[24] = vref;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(info_full + 8 * (j & 3));
+      }
+      slots = slots_of(j + 1);
+      if (j + 1 < n_tiles) load(c.k_codes, j + 1, slots, kx);
+      if (j >= 2 && !wait(v_empty + 8 * st, ((j - 2) >> 1) & 1)) break;
+      put(smem + C::kOffV + st * C::kKVBytes, vx);
+      mbar_arrive(v_full + 8 * st);
+    }
+  } else if (warp == kIssueWarp && lane == 0) {
+    // ---------------------------------------------------------- issue
+    constexpr uint32_t kIdS = instr_desc(kBN, false), kIdO = instr_desc(D, true);
+    bool ok = true;
+    auto issue_s = [&](int i) {
+      const int j = i / nt, t = i - j * nt, st = j & 1;
+      if (t == 0) ok = wait1(k_full + 8 * st, (j >> 1) & 1);
+      if (!ok) return;
+      t5_after();
+      const uint32_t d = tmem + C::kColS + (i & 1) * kBN;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ks++) {
+        const uint32_t at = (ks & 3) * 32;
+        const uint64_t qa = smem_desc(base + t * C::kQTileBytes + (ks >> 2) * (128 * 128) + at, 16, 1024);
+        const uint64_t kb =
+            smem_desc(base + C::kOffK + st * C::kKVBytes + (ks >> 2) * (kBN * 128) + at, 16, 1024);
+        t5_mma_ss(d, qa, kb, kIdS, ks > 0);
+      }
+      t5_commit(s_full + 8 * (i & 1));
+      if (t == nt - 1) t5_commit(k_empty + 8 * st);
+    };
+    for (int i = 0; i < min(2, n_items) && ok; i++) issue_s(i);
+    for (int i = 0; i < n_items && ok; i++) {
+      const int j = i / nt, t = i - j * nt, st = j & 1;
+      ok = wait1(p_full + 8 * (i & 1), (i >> 1) & 1);
+      if (ok && t == 0) ok = wait1(v_full + 8 * st, (j >> 1) & 1);
+      if (!ok) break;
+      t5_after();
+      const uint32_t p = tmem + C::kColS + (i & 1) * kBN;
+#pragma unroll
+      for (int ks = 0; ks < kBN / 16; ks++) {
+        const uint64_t vb = smem_desc(base + C::kOffV + st * C::kKVBytes + ks * 2048, kBN * 128, 1024);
+        t5_mma_ts(tmem + C::kColO + t * D, p + 8 * ks, vb, kIdO, j > 0 || ks > 0);
+      }
+      t5_commit(o_done + 8 * t);
+      if (t == nt - 1) t5_commit(v_empty + 8 * st);
+      if (i + 2 < n_items) issue_s(i + 2);
+    }
+    if (!ok) {
+      // products may be in flight: they end before tensor memory is given back
+      // (a bounded wait, like every other)
+      t5_commit(drain);
+      for (int n = 0; n < (1 << 20) && !dec::mbar_try(drain, 0); n++) {
+      }
+    }
+  }
+  __syncwarp();
+  t5_before();
+  __syncthreads();
+  if (warp == kIssueWarp) {
+    t5_after();
+    t5_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
+  using C = PCfg<D>;
+  const cudaError_t e = cudaFuncSetAttribute(b8_prefill_kernel<D>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t units = (int64_t)a.q.batch * a.c.num_kv_heads * a.p.row_tiles;
+  b8_prefill_kernel<D><<<(unsigned)(units * a.p.splits), C::kThreads, C::kSmem, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int b8_prefill_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }
+int b8_prefill_tokens(int head_dim) { return head_dim == 256 ? 64 : 128; }
+
+cudaError_t launch_b8_prefill(const AttnArgs &a, cudaStream_t s) {
+  switch (a.c.head_dim) {
+    case 64: return launch<64>(a, s);
+    case 128: return launch<128>(a, s);
+    default: return launch<256>(a, s);
+  }
+}
+
+}  // namespace kvq

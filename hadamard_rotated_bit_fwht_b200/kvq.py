@@ -156,7 +156,7 @@ def lib():
         L.kvq_b8_gather.argtypes = [C.POINTER(B8CacheDesc), C.c_int32, C.c_void_p, C.c_void_p,
                                     C.c_int32, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p]
         L.kvq_b8_attn_workspace.restype = C.c_size_t
-        L.kvq_b8_attn_workspace.argtypes = [C.POINTER(B8CacheDesc)] + [C.c_int32] * 4
+        L.kvq_b8_attn_workspace.argtypes = [C.POINTER(B8CacheDesc), C.c_int] + [C.c_int32] * 4
         L.kvq_b8_attn.argtypes = [C.POINTER(B8CacheDesc), C.POINTER(B8QueriesDesc), C.c_void_p,
                                   C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]
         L.kvq_b8_attn_mass.argtypes = [C.POINTER(B8CacheDesc), C.POINTER(B8QueriesDesc),
@@ -771,8 +771,10 @@ def _b8_queries(cache, q, seq_lens, max_seq_len, scale, cu_q, max_q) -> B8Querie
 
 
 def b8_attn_workspace(cache: B8Cache, batch: int, num_q_heads: int, max_seq_len: int,
-                      max_q: int = 1) -> int:
-    return int(lib().kvq_b8_attn_workspace(C.byref(cache.desc()), num_q_heads, batch, max_q,
+                      max_q: int = 1, dtype: torch.dtype = torch.bfloat16) -> int:
+    """Bytes of workspace that b8_attn needs for queries of this dtype."""
+    code = KVQ_BF16 if dtype == torch.bfloat16 else KVQ_F32
+    return int(lib().kvq_b8_attn_workspace(C.byref(cache.desc()), code, num_q_heads, batch, max_q,
                                            max_seq_len))
 
 
@@ -795,7 +797,7 @@ def b8_attn(cache: B8Cache, q: torch.Tensor, seq_lens: torch.Tensor, max_seq_len
                             or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous fp32 [queries, Hq] tensor")
     if workspace is None:
-        n = b8_attn_workspace(cache, d.batch, q.shape[1], d.max_seq_len, d.max_q)
+        n = b8_attn_workspace(cache, d.batch, q.shape[1], d.max_seq_len, d.max_q, q.dtype)
         if n:
             workspace = _empty(n, torch.uint8, q, stream)
     _here(cache=cache.k_codes, q=q, seq_lens=seq_lens, cu_q=cu_q, out=out, lse=lse,

@@ -462,8 +462,8 @@ KVQ_API kvq_status kvq_rope(const kvq_rope_spec *spec, kvq_dtype dtype, int32_t 
  * rotation is applied, so any head_dim of 64, 128 or 256 serves.
  *   k_codes / v_codes   [num_blocks][num_kv_heads][block_size][head_dim] int8,
  *                       16-byte aligned;
- *   k_scales / v_scales [num_blocks][num_kv_heads] fp32; a block whose scale
- *                       is 0 holds zero codes.
+ *   k_scales / v_scales [num_blocks][num_kv_heads] fp32, finite and >= 0; a
+ *                       block whose scale is 0 holds zero codes.
  * Token t of sequence b lies in block block_table[b][t / block_size] at row
  * t % block_size.  Table entries outside [0, num_blocks) are unmapped: appends
  * skip them, reads give zeros and attention leaves their tokens out. */
@@ -545,8 +545,9 @@ typedef struct {
  * and an lse of -inf.  Products are accurate to fp32 for KVQ_F32 queries (22
  * bits of q and of the probabilities); for KVQ_BF16 q is exact and the
  * probabilities are rounded to 11 bits before they meet V. */
-KVQ_API size_t kvq_b8_attn_workspace(const kvq_b8_cache *cache, int32_t num_q_heads,
-                                     int32_t batch, int32_t max_q, int32_t max_seq_len);
+KVQ_API size_t kvq_b8_attn_workspace(const kvq_b8_cache *cache, kvq_dtype dtype,
+                                     int32_t num_q_heads, int32_t batch, int32_t max_q,
+                                     int32_t max_seq_len);
 KVQ_API kvq_status kvq_b8_attn(const kvq_b8_cache *cache, const kvq_b8_queries *queries,
                                void *out, float *lse, void *workspace, size_t workspace_bytes,
                                void *stream);
