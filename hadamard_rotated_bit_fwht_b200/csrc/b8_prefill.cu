@@ -43,7 +43,9 @@ struct PCfg {
   static constexpr int kInfo = 4;                 // slots of group constants
   static constexpr int kOffK = kNT * kQTileBytes;
   static constexpr int kOffV = kOffK + 2 * kKVBytes;
-  static constexpr int kOffInfo = kOffV + 2 * kKVBytes;
+  static constexpr int kRawBytes = kBN * D;       // codes of a K or V tile as they come
+  static constexpr int kOffRaw = kOffV + 2 * kKVBytes;
+  static constexpr int kOffInfo = kOffRaw + 2 * kRawBytes;
   static constexpr int kInfoFloats = 3 * 8 + 4;   // k factor, log2 v factor, its inverse; vref
   static constexpr int kOffBar = kOffInfo + kInfo * kInfoFloats * 4;
   // k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2],
@@ -98,22 +100,28 @@ __device__ __forceinline__ void t5_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
 }
 // 32 columns of this thread's lane
 __device__ __forceinline__ void t5_ld32(uint32_t addr, float (&v)[32]) {
-  uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
       "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]),
+        "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+        "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(addr));
-#pragma unroll
-  for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void t5_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// The loads are asynchronous: their registers hold nothing before this wait.
+// It takes them as operands, so that no use moves in front of it.
+__device__ __forceinline__ void t5_wait_ld(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+        "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
+        "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]),
+        "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]),
+        "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+      :
+      : "memory");
 }
 __device__ __forceinline__ void t5_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -146,6 +154,54 @@ __device__ __forceinline__ void widen16(const uint4 &w, uint4 (&h)[2]) {
   k_frag(w.y, h[0].z, h[0].w);
   k_frag(w.z, h[1].x, h[1].y);
   k_frag(w.w, h[1].z, h[1].w);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// raise mx to the largest score of two 16-token groups; in: their constants
+__device__ __forceinline__ void group_max(const float (&s)[32], const float *in, float inv,
+                                          float &mx) {
+#pragma unroll
+  for (int gr = 0; gr < 2; gr++) {
+    const float *x = s + 16 * gr;
+    float g0 = fmaxf(x[0], x[1]), g1 = fmaxf(x[2], x[3]);
+#pragma unroll
+    for (int e = 4; e < 16; e += 4) {
+      g0 = max3(g0, x[e], x[e + 1]);
+      g1 = max3(g1, x[e + 2], x[e + 3]);
+    }
+    // unmapped groups have a log2 factor of -inf
+    const float y = fmaxf(g0, g1) * (inv * in[gr]);
+    mx = fmaxf(mx, in[8 + gr] == -INFINITY ? -INFINITY : y);
+  }
+}
+// two groups of scores -> p' as fp16 at `to`; l grows by their probabilities
+template <bool CUT>
+__device__ __forceinline__ void group_exp(const float (&s)[32], const float *in, float inv, float m,
+                                          int left, float &l, uint32_t to) {
+  uint32_t w[16];
+#pragma unroll
+  for (int gr = 0; gr < 2; gr++) {
+    const float f = inv * in[gr], c = in[8 + gr] - m;
+    const float2 f2 = make_float2(f, f), c2 = make_float2(c, c);
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      const float2 x = __ffma2_rn(make_float2(s[16 * gr + e], s[16 * gr + e + 1]), f2, c2);
+      float2 p = make_float2(ex2(x.x), ex2(x.y));
+      if (CUT) {
+        p.x = 16 * gr + e < left ? p.x : 0.f;
+        p.y = 16 * gr + e + 1 < left ? p.y : 0.f;
+      }
+      sum = add2(sum, p);
+      w[8 * gr + e / 2] = pack_f16x2(p.x, p.y);
+    }
+    l = fmaf(sum.x + sum.y, in[16 + gr], l);
+  }
+  t5_st16(to, w);
 }
 
 template <int D>
@@ -282,29 +338,28 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       const bool cut = __any_sync(0xffffffffu, tok + kBN > lim);
       // row maximum
       float mx = -INFINITY;
+      if (!cut) {
+        float s0[32], s1[32];
+        t5_ld32(s_at, s0);
+#pragma unroll 1
+        for (int ch = 0; ch < kBN / 32; ch += 2) {
+          t5_wait_ld(s0);
+          t5_ld32(s_at + 32 * ch + 32, s1);
+          group_max(s0, in + 2 * ch, inv, mx);
+          t5_wait_ld(s1);
+          if (ch + 2 < kBN / 32) t5_ld32(s_at + 32 * ch + 64, s0);
+          group_max(s1, in + 2 * ch + 2, inv, mx);
+        }
+      } else {
+#pragma unroll 1
+        for (int ch = 0; ch < kBN / 32; ch++) {
+          float s[32];
+          t5_ld32(s_at + 32 * ch, s);
+          t5_wait_ld(s);
 #pragma unroll
-      for (int ch = 0; ch < kBN / 32; ch++) {
-        float s[32];
-        t5_ld32(s_at + 32 * ch, s);
-        t5_wait_ld();
-#pragma unroll
-        for (int gr = 0; gr < 2; gr++) {
-          const float f = inv * in[2 * ch + gr];
-          // unmapped groups have a log2 factor of -inf
-          const float bias = in[8 + 2 * ch + gr] == -INFINITY ? -INFINITY : 0.f;
-          if (cut) {
-            const int left = lim - (tok + 32 * ch + 16 * gr);
-#pragma unroll
-            for (int e = 0; e < 16; e++)
-              mx = fmaxf(mx, e < left ? fmaf(s[16 * gr + e], f, bias) : -INFINITY);
-          } else {
-            float g0 = s[16 * gr], g1 = s[16 * gr + 1];
-#pragma unroll
-            for (int e = 2; e < 16; e += 2) {
-              g0 = fmaxf(g0, s[16 * gr + e]);
-              g1 = fmaxf(g1, s[16 * gr + e + 1]);
-            }
-            mx = fmaxf(mx, fmaf(fmaxf(g0, g1), f, bias));
+          for (int e = 0; e < 32; e++) {
+            const float y = s[e] * (inv * in[2 * ch + e / 16]);
+            if (tok + 32 * ch + e < lim && in[8 + 2 * ch + e / 16] != -INFINITY) mx = fmaxf(mx, y);
           }
         }
       }
@@ -326,7 +381,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
           for (int ch = 0; ch < D / 32; ch++) {
             float o[32];
             t5_ld32(o_at + 32 * ch, o);
-            t5_wait_ld();
+            t5_wait_ld(o);
 #pragma unroll
             for (int h = 0; h < 2; h++) {
               uint32_t w[16];
@@ -339,38 +394,35 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
         vref = nref;
       }
       // probabilities, over the scores that were read
-#pragma unroll
-      for (int ch = 0; ch < kBN / 32; ch++) {
-        float s[32];
-        t5_ld32(s_at + 32 * ch, s);
-        t5_wait_ld();
-        uint32_t w[16];
-#pragma unroll
-        for (int gr = 0; gr < 2; gr++) {
-          const float f = inv * in[2 * ch + gr], cst = in[8 + 2 * ch + gr] - m;
-          const int left = cut ? lim - (tok + 32 * ch + 16 * gr) : 16;
-          float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float p0 = ex2(fmaf(s[16 * gr + e], f, cst));
-            float p1 = ex2(fmaf(s[16 * gr + e + 1], f, cst));
-            if (cut) {
-              p0 = e < left ? p0 : 0.f;
-              p1 = e + 1 < left ? p1 : 0.f;
-            }
-            sum0 += p0;
-            sum1 += p1;
-            w[8 * gr + e / 2] = pack_f16x2(p0, p1);
-          }
-          l = fmaf(sum0 + sum1, in[16 + 2 * ch + gr], l);
+      if (!cut) {
+        float s0[32], s1[32];
+        t5_ld32(s_at, s0);
+#pragma unroll 1
+        for (int ch = 0; ch < kBN / 32; ch += 2) {
+          t5_wait_ld(s0);
+          t5_ld32(s_at + 32 * ch + 32, s1);
+          group_exp<false>(s0, in + 2 * ch, inv, m, 0, l, s_at + 16 * ch);
+          t5_wait_ld(s1);
+          if (ch + 2 < kBN / 32) t5_ld32(s_at + 32 * ch + 64, s0);
+          group_exp<false>(s1, in + 2 * ch + 2, inv, m, 0, l, s_at + 16 * ch + 16);
         }
-        t5_st16(s_at + 16 * ch, w);
+      } else {
+#pragma unroll 1
+        for (int ch = 0; ch < kBN / 32; ch++) {
+          float s[32];
+          t5_ld32(s_at + 32 * ch, s);
+          t5_wait_ld(s);
+          group_exp<true>(s, in + 2 * ch, inv, m, lim - tok - 32 * ch, l, s_at + 16 * ch);
+        }
       }
       t5_wait_st();
       t5_before();
       mbar_arrive(p_full + 8 * buf);
     }
     // ---- result
+    // (a wait tells a phase from the next one only: with one row tile the last
+    // score tile says that product n - 3 is done, so n - 2 comes first)
+    if (ok && n_tiles > 1) ok = wait(o_done + 8 * wg, (n_tiles - 2) & 1);
     if (ok && n_tiles > 0) ok = wait(o_done + 8 * wg, (n_tiles - 1) & 1);
     t5_after();
     const bool direct = a.p.splits == 1;
@@ -387,7 +439,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       __syncwarp();
       if (n_tiles > 0) {
         t5_ld32(o_at + 32 * ch, o);
-        t5_wait_ld();
+        t5_wait_ld(o);
       } else {
 #pragma unroll
         for (int e = 0; e < 32; e++) o[e] = 0.f;
@@ -426,58 +478,74 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
     constexpr int kPer = kBN * D / 16 / 128;  // 16-code pieces a thread has of a tile
     const int ct = tid - C::kSoft;
     const int32_t *table = c.block_table + (int64_t)b * c.max_blocks_per_seq;
+    const int bs = c.block_size, shift = __ffs(bs) - 1;
     // lane l: block of 16-token group l % kGroups of tile j, -1 if unmapped or
     // past the range
     auto slots_of = [&](int j) {
       const int t = t0 + j * kBN + (lane % C::kGroups) * 16;
       int p = -1;
       if (j < n_tiles && t < t1) {
-        p = __ldg(table + t / c.block_size);
+        p = __ldg(table + (t >> shift));
         if (p < 0 || p >= c.num_blocks || !in_bounds(p, p + 1, c.num_blocks, a.err)) p = -1;
       }
       return p;
     };
-    // piece i of this thread: plane (64 dims) pl, token tr, 16 dims 16 cc
-    auto load = [&](const int8_t *codes, int j, int slots, uint4 (&x)[kPer]) {
+    // a thread copies and converts the same pieces, so the raw bytes need no
+    // barrier: piece i is token 32 (i % kTr) + ct / 4, dims 64 (i / kTr) +
+    // 16 (ct % 4) .. + 15
+    constexpr int kTr = kBN / 32;
+    const int r4 = ct >> 2, c4 = ct & 3;
+    auto copy = [&](const int8_t *codes, uint32_t raw, int j, int slots) {
+      // first code of the lane's group
+      const int t = t0 + j * kBN + (lane % C::kGroups) * 16;
+      int64_t off = -1;
+      if (slots >= 0)
+        off = ((((int64_t)slots * c.num_kv_heads + kvh) << shift) + (t & (bs - 1))) * D;
 #pragma unroll
-      for (int i = 0; i < kPer; i++) {
-        const int p = ct + 128 * i, pl = p / (4 * kBN), tr = (p >> 2) % kBN, cc = p & 3;
-        const int slot = __shfl_sync(0xffffffffu, slots, tr >> 4);
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (slot >= 0) {
-          const int at = (t0 + j * kBN + tr) % c.block_size;
-          x[i] = ldg_stream_u4(codes + (((int64_t)slot * c.num_kv_heads + kvh) * c.block_size + at) * D +
-                               64 * pl + 16 * cc);
+      for (int i = 0; i < kTr; i++) {
+        const int tr = 32 * i + r4;
+        const int64_t o = __shfl_sync(0xffffffffu, off, tr >> 4);
+        const int8_t *src = codes + o + (tr & 15) * D + 16 * c4;
+#pragma unroll
+        for (int pl = 0; pl < D / 64; pl++) {
+          const uint32_t dst = raw + (((pl * kTr + i) * 128 + ct) << 4);
+          if (o >= 0)
+            cp_async16(dst, src + 64 * pl);
+          else
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0) : "memory");
         }
       }
+      cp_commit();
     };
-    auto put = [&](uint8_t *dst, const uint4 (&x)[kPer]) {
+    auto put = [&](uint8_t *dst, const uint8_t *raw) {
 #pragma unroll
       for (int i = 0; i < kPer; i++) {
-        const int p = ct + 128 * i, pl = p / (4 * kBN), tr = (p >> 2) % kBN, cc = p & 3;
+        const int tr = 32 * (i % kTr) + r4;
         uint4 h[2];
-        widen16(x[i], h);
-        uint8_t *at = dst + pl * (kBN * 128) + tr * 128;
-        *reinterpret_cast<uint4 *>(at + (((2 * cc) ^ (tr & 7)) << 4)) = h[0];
-        *reinterpret_cast<uint4 *>(at + (((2 * cc + 1) ^ (tr & 7)) << 4)) = h[1];
+        widen16(*reinterpret_cast<const uint4 *>(raw + ((i * 128 + ct) << 4)), h);
+        uint8_t *at = dst + (i / kTr) * (kBN * 128) + tr * 128;
+        *reinterpret_cast<uint4 *>(at + (((2 * c4) ^ (tr & 7)) << 4)) = h[0];
+        *reinterpret_cast<uint4 *>(at + (((2 * c4 + 1) ^ (tr & 7)) << 4)) = h[1];
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     };
+    const uint8_t *kraw = smem + C::kOffRaw, *vraw = kraw + C::kRawBytes;
     float vref = 0x1p-100f;
-    int slots = slots_of(0);
-    uint4 kx[kPer], vx[kPer];
-    if (n_tiles > 0) load(c.k_codes, 0, slots, kx);
-    for (int j = 0; j < n_tiles; j++) {
-      const int st = j & 1;
-      load(c.v_codes, j, slots, vx);
-      float ks = 0.f, vs = 0.f;
+    int slots = slots_of(0), next = slots_of(1);
+    copy(c.k_codes, smem_u32(kraw), 0, slots);
+    copy(c.v_codes, smem_u32(vraw), 0, slots);
+    auto scales_of = [&](int slots, float &ks, float &vs) {
+      ks = vs = 0.f;
       if (warp == C::kSoft / 32 && slots >= 0) {
         ks = __ldg(c.k_scales + (int64_t)slots * c.num_kv_heads + kvh);
         vs = __ldg(c.v_scales + (int64_t)slots * c.num_kv_heads + kvh);
       }
-      if (j >= 2 && !wait(k_empty + 8 * st, ((j - 2) >> 1) & 1)) break;
-      put(smem + C::kOffK + st * C::kKVBytes, kx);
-      mbar_arrive(k_full + 8 * st);
+    };
+    float ks, vs;
+    scales_of(slots, ks, vs);
+    for (int j = 0; j < n_tiles; j++) {
+      const int st = j & 1;
+      const int after = slots_of(j + 2);
       if (warp == C::kSoft / 32) {
         // the tile's group constants; slot j % 4 was last read for tile j - 4,
         // whose second product was waited for before V of tile j - 2 was stored
@@ -501,12 +569,21 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(info_full + 8 * (j & 3));
       }
-      slots = slots_of(j + 1);
-      if (j + 1 < n_tiles) load(c.k_codes, j + 1, slots, kx);
+      cp_wait<1>();
+      if (j >= 2 && !wait(k_empty + 8 * st, ((j - 2) >> 1) & 1)) break;
+      put(smem + C::kOffK + st * C::kKVBytes, kraw);
+      mbar_arrive(k_full + 8 * st);
+      copy(c.k_codes, smem_u32(kraw), j + 1, next);
+      scales_of(next, ks, vs);
+      cp_wait<1>();
       if (j >= 2 && !wait(v_empty + 8 * st, ((j - 2) >> 1) & 1)) break;
-      put(smem + C::kOffV + st * C::kKVBytes, vx);
+      put(smem + C::kOffV + st * C::kKVBytes, vraw);
       mbar_arrive(v_full + 8 * st);
+      copy(c.v_codes, smem_u32(vraw), j + 1, next);
+      slots = next;
+      next = after;
     }
+    cp_wait<0>();
   } else if (warp == kIssueWarp && lane == 0) {
     // ---------------------------------------------------------- issue
     constexpr uint32_t kIdS = instr_desc(kBN, false), kIdO = instr_desc(D, true);
