@@ -173,6 +173,9 @@ kvq_status kvq_b8_gather(const kvq_b8_cache *cache, int32_t batch, const int32_t
   if (batch == 0 || count == 0) return KVQ_OK;
   if (!d_first || !d_ends || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16))
     return KVQ_ERR_INVALID_ARG;
+  // 8-element pieces of a sequence in 32 bits, sequences on a grid axis
+  if ((int64_t)count * cache->num_kv_heads * (cache->head_dim / 8) >= (1LL << 31) || batch > 65535)
+    return KVQ_ERR_UNSUPPORTED;
   return from_cuda(launch_b8_gather(*cache, batch, d_first, d_ends, count, dtype == KVQ_BF16,
                                     k_out, v_out, as_stream(stream)));
 }

@@ -24,14 +24,14 @@ __device__ __forceinline__ float inverse(float scale) {
   return scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
 }
 
-// rint(x * inv) of 4 values, clamped to [-127, 127], as packed bytes.  The sum
-// with 1.5 * 2^23 rounds to the nearest even integer and leaves it in the low
-// byte; NaN products (an infinite input times 0) come out as some code.
+// rint(x) of 4 values as packed bytes.  The sum with 1.5 * 2^23 rounds to the
+// nearest even integer and leaves it in the low byte.  No clamp is needed:
+// scale >= RN(amax / 127) and |x| <= amax give |x * RN(1 / scale)| <= 127 (1 +
+// 2^-22), which rounds to 127, and old codes shrink.  NaN products (an infinite
+// input times 0) come out as some code.
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
   constexpr float kMagic = 12582912.f;
-  auto one = [](float x) {
-    return __float_as_uint(__fadd_rn(fminf(fmaxf(x, -127.f), 127.f), kMagic));
-  };
+  auto one = [](float x) { return __float_as_uint(__fadd_rn(x, kMagic)); };
   return __byte_perm(__byte_perm(one(a), one(b), 0x0040), __byte_perm(one(c), one(d), 0x0040),
                      0x5410);
 }

@@ -6,8 +6,8 @@
 // Selection: one CTA per (sequence, kv head) finds the k-th largest weight by
 // a radix select over order-preserving 32-bit keys (digits of 11, 11 and 10
 // bits, counted in shared memory), then walks the tokens in order and writes
-// the kept indices where a prefix sum puts them.  Requantization: one CTA per
-// kept block of a head and plane; rows are held in registers between the
+// the kept indices where a prefix sum puts them.  Requantization: a warp
+// or a CTA per kept block of a head; rows are held in registers between the
 // block's maximum and the rounding, so kept codes are read once.  Bound: HBM.
 #include "b8_common.cuh"
 
@@ -43,7 +43,9 @@ __device__ __forceinline__ int evict_len(const EvictArgs &a, int b) {
 }
 
 // grid: kv head + heads * sequence
-__global__ void __launch_bounds__(kSelThreads) b8_select_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kSelThreads)
+    b8_select_kernel(const __grid_constant__ EvictArgs a, int cached) {
+  extern __shared__ uint32_t keys[];  // of the first `cached` tokens
   __shared__ int bins[kBins];
   __shared__ int wsum[2][kWarps];
   __shared__ int found[2];  // digit, elements above it
@@ -64,6 +66,12 @@ __global__ void __launch_bounds__(kSelThreads) b8_select_kernel(const __grid_con
   const int lo = a.sinks, hi = n - a.recent;  // the tokens that compete
   const int k = m - a.sinks - a.recent;       // how many of them stay, < hi - lo
 
+  const int nc = min(n, cached);
+#pragma unroll 8
+  for (int i = tid; i < nc; i += kSelThreads) keys[i] = order_key(w[i]);
+  __syncthreads();
+  auto key_of = [&](int i) { return i < nc ? keys[i] : order_key(w[i]); };
+
   // the k-th largest key `prefix`, and how many of its equals stay
   uint32_t prefix = 0, mask = 0;
   int need = k;
@@ -76,7 +84,7 @@ __global__ void __launch_bounds__(kSelThreads) b8_select_kernel(const __grid_con
       __syncthreads();
 #pragma unroll 8
       for (int i = lo + tid; i < hi; i += kSelThreads) {
-        const uint32_t key = order_key(w[i]);
+        const uint32_t key = key_of(i);
         if ((key & mask) == prefix) atomicAdd(&bins[key >> shift & (nb - 1)], 1);
       }
       __syncthreads();
@@ -111,7 +119,7 @@ __global__ void __launch_bounds__(kSelThreads) b8_select_kernel(const __grid_con
     if (i >= r1) return 0;
     if (i < lo || i >= hi) return 2;
     if (k == 0) return 0;
-    const uint32_t key = order_key(w[i]);
+    const uint32_t key = key_of(i);
     return key > prefix ? 2 : key == prefix ? 1 : 0;
   };
   int over = 0, equal = 0;
@@ -141,82 +149,159 @@ __global__ void __launch_bounds__(kSelThreads) b8_select_kernel(const __grid_con
   }
 }
 
-constexpr int kItems = 4;  // 16-code pieces a thread holds
+// A block of a head is 1 to 16 runs of 4 KB a plane; one warp holds its run of
+// K and V (8 16-byte pieces a lane and plane) in registers between the block's
+// maximum and the rounding.  Warps walk many blocks: while the codes of one are
+// on their way, the scales and table entries of the next one's rows and the
+// kept indices of the one after are too (a row or two a lane), so that the
+// chain index -> block -> scale costs no time of its own.
+constexpr int kItems = 8;
 
-// grid: plane (K, V) + 2 * (kept block + cols * (kv head + heads * sequence))
-template <int kMost>
-__global__ void __launch_bounds__(kMost) b8_requant_kernel(const __grid_constant__ EvictArgs a, int cols) {
-  __shared__ float warp_max[32];
-  int u = blockIdx.x;
-  const bool is_v = u & 1;
-  u >>= 1;
-  const int col = u % cols;
-  u /= cols;  // (sequence, kv head)
-  const int hkv = a.src.num_kv_heads, h = u % hkv, b = u / hkv;
-  const int bs = a.dst.block_size, D = a.dst.head_dim;
-  const int rows = min(bs, min(evict_len(a, b), a.keep) - col * bs);
-  if (rows <= 0) return;
-  const int64_t to = b8::block_of(a.dst, b, col);
-  if (to < 0 || !in_bounds(to, to + 1, a.dst.num_blocks, a.err)) return;
-  const int32_t *kept = a.kept + (int64_t)u * a.keep + (int64_t)col * bs;
-  const int8_t *codes = is_v ? a.src.v_codes : a.src.k_codes;
-  const float *scales = is_v ? a.src.v_scales : a.src.k_scales;
-  const int pieces = D / 16, items = rows * pieces;
-  uint4 raw[kItems];
-  float sc[kItems];
-  float amax = 0.f;
+// Blocks of one run: a warp each.  Larger ones: a CTA of `runs` warps each.
+// unit: kept block + cols * (kv head + heads * sequence)
+template <int D>
+__global__ void __launch_bounds__(512)
+    b8_requant_kernel(const __grid_constant__ EvictArgs a, int cols, int runs, int64_t units) {
+  __shared__ float warp_max[2][2][16];
+  constexpr int kPieces = D / 16, kRows = 4096 / D, kMine = (kRows + 31) / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int run = runs > 1 ? warp : 0, r0 = run * kRows;
+  const int64_t stride = runs > 1 ? gridDim.x : (int64_t)gridDim.x * (blockDim.x / 32);
+  int64_t unit = runs > 1 ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x / 32) + warp;
+  const int hkv = a.src.num_kv_heads;
+  const int bs = a.dst.block_size, sbs = a.src.block_size, shift = __ffs(sbs) - 1;
+
+  // kept index of the lane's row i of a unit's run, -1 if there is none
+  auto load_kept = [&](int64_t u, int (&t)[kMine]) {
 #pragma unroll
-  for (int i = 0; i < kItems; i++) {
-    const int it = threadIdx.x + i * blockDim.x;
-    raw[i] = make_uint4(0, 0, 0, 0);
-    sc[i] = 0.f;
-    if (it < items) {
-      const int r = it / pieces, t = kept[r];
-      const int64_t slot = b8::block_of(a.src, b, t / a.src.block_size);
-      if (slot >= 0 && in_bounds(slot, slot + 1, a.src.num_blocks, a.err)) {
-        const int64_t sh = slot * hkv + h;
-        raw[i] = *reinterpret_cast<const uint4 *>(
-            codes + (sh * a.src.block_size + t % a.src.block_size) * D + 16 * (it - r * pieces));
-        sc[i] = scales[sh];
+    for (int i = 0; i < kMine; i++) t[i] = -1;
+    if (u >= units) return;
+    const int64_t bh = u / cols;
+    const int row0 = (int)(u - bh * cols) * bs + r0;
+#pragma unroll
+    for (int i = 0; i < kMine; i++) {
+      const int r = lane + 32 * i;
+      // entries behind the last kept token are -1
+      if (r < kRows && r0 + r < bs && row0 + r < a.keep) t[i] = __ldcg(a.kept + bh * a.keep + row0 + r);
+    }
+  };
+  // its block and, on lane 0, the block that the unit goes to
+  auto load_slots = [&](int64_t u, const int (&t)[kMine], int (&slot)[kMine], int &to) {
+    to = -1;
+    if (u >= units) return;
+    const int64_t bh = u / cols;
+    const int b = (int)(bh / hkv);
+#pragma unroll
+    for (int i = 0; i < kMine; i++)
+      slot[i] = t[i] < 0 ? -1 : (int)b8::block_of(a.src, b, t[i] >> shift);
+    to = (int)b8::block_of(a.dst, b, (int)(u - bh * cols));
+  };
+  int t[kMine], slot[kMine], to;
+  load_kept(unit, t);
+  load_slots(unit, t, slot, to);
+  int t2[kMine];
+  load_kept(unit + stride, t2);
+  int parity = 0;
+  for (; unit < units; unit += stride, parity ^= 1) {
+    const int64_t bh = unit / cols;
+    const int h = (int)(bh % hkv);
+    int64_t src[kMine];
+    float ks[kMine], vs[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; i++) {
+      src[i] = -1;
+      ks[i] = vs[i] = 0.f;
+      if (slot[i] >= 0 && in_bounds(slot[i], slot[i] + 1, a.src.num_blocks, a.err)) {
+        const int64_t sh = (int64_t)slot[i] * hkv + h;
+        src[i] = ((sh << shift) + (t[i] & (sbs - 1))) * D;
+        ks[i] = a.src.k_scales[sh];
+        vs[i] = a.src.v_scales[sh];
       }
     }
-  }
+    const int dst = to;
+    // rows of the run that are kept (an unmapped source stores zeros)
+    uint32_t has[kMine];
 #pragma unroll
-  for (int i = 0; i < kItems; i++) {
-    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    for (int i = 0; i < kMine; i++) has[i] = __ballot_sync(0xffffffffu, t[i] >= 0);
+    uint4 raw[2][kItems];
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      float x[4];
-      b8::decode4(w[j], sc[i], x);
-#pragma unroll
-      for (int e = 0; e < 4; e++) amax = fmaxf(amax, fabsf(x[e]));
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
-  __syncthreads();
-  for (int w = 0; w < (int)blockDim.x / 32; w++) amax = fmaxf(amax, warp_max[w]);
-  const float scale = b8::scale_of(amax), inv = b8::inverse(scale);
-  const int64_t dh = to * hkv + h;
-  int8_t *out = (is_v ? a.dst.v_codes : a.dst.k_codes) + dh * bs * D;
-#pragma unroll
-  for (int i = 0; i < kItems; i++) {
-    const int it = threadIdx.x + i * blockDim.x;
-    if (it < items) {
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        float x[4];
-        b8::decode4(w[j], sc[i], x);
-        o[j] = b8::encode4(__fmul_rn(x[0], inv), __fmul_rn(x[1], inv), __fmul_rn(x[2], inv),
-                           __fmul_rn(x[3], inv));
+    for (int i = 0; i < kItems; i++) {
+      // row of the run; whether it is one of the lanes' first or second rows
+      // goes by i alone
+      const int r = (lane + 32 * i) / kPieces;
+      const int64_t at = __shfl_sync(0xffffffffu, src[32 * i / kPieces / 32], r & 31);
+      raw[0][i] = raw[1][i] = make_uint4(0, 0, 0, 0);
+      if (at >= 0) {
+        raw[0][i] = *reinterpret_cast<const uint4 *>(a.src.k_codes + at + 16 * (lane % kPieces));
+        raw[1][i] = *reinterpret_cast<const uint4 *>(a.src.v_codes + at + 16 * (lane % kPieces));
       }
-      *reinterpret_cast<uint4 *>(out + 16 * (int64_t)it) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    // the next units' indices
+#pragma unroll
+    for (int i = 0; i < kMine; i++) t[i] = t2[i];
+    load_slots(unit + stride, t, slot, to);
+    load_kept(unit + 2 * stride, t2);
+
+    float amax[2] = {0.f, 0.f};
+#pragma unroll
+    for (int p = 0; p < 2; p++)
+#pragma unroll
+      for (int i = 0; i < kItems; i++) {
+        const float sc = __shfl_sync(0xffffffffu, (p ? vs : ks)[32 * i / kPieces / 32],
+                                     (lane + 32 * i) / kPieces & 31);
+        const uint32_t w[4] = {raw[p][i].x, raw[p][i].y, raw[p][i].z, raw[p][i].w};
+        // the largest magnitude of the codes (rounding keeps the order)
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 4; j++) m = __vmaxu4(m, __vabs4(w[j]));
+        m = __vmaxu4(m, m >> 16);
+        m = __vmaxu4(m, m >> 8) & 0xff;
+        amax[p] = fmaxf(amax[p], __fmul_rn((float)m, sc));
+      }
+#pragma unroll
+    for (int p = 0; p < 2; p++)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        amax[p] = fmaxf(amax[p], __shfl_xor_sync(0xffffffffu, amax[p], o));
+    if (runs > 1) {
+      // two sets, so that one barrier a unit is enough
+      if (lane == 0) warp_max[parity][0][warp] = amax[0], warp_max[parity][1][warp] = amax[1];
+      __syncthreads();
+      for (int w = 0; w < runs; w++) {
+        amax[0] = fmaxf(amax[0], warp_max[parity][0][w]);
+        amax[1] = fmaxf(amax[1], warp_max[parity][1][w]);
+      }
+    }
+    // a block without kept tokens, or one that is not mapped, is left alone
+    const int first = (int)(unit - bh * cols) * bs;
+    const bool store = dst >= 0 && first < min(evict_len(a, (int)(bh / hkv)), a.keep) &&
+                       in_bounds(dst, (int64_t)dst + 1, a.dst.num_blocks, a.err);
+    if (!store) continue;
+    const int64_t dh = (int64_t)dst * hkv + h;
+#pragma unroll
+    for (int p = 0; p < 2; p++) {
+      const float scale = b8::scale_of(amax[p]), inv = b8::inverse(scale);
+      int8_t *out = (p ? a.dst.v_codes : a.dst.k_codes) + (dh * bs + r0) * D;
+#pragma unroll
+      for (int i = 0; i < kItems; i++) {
+        const int r = (lane + 32 * i) / kPieces;
+        const float sc =
+            __shfl_sync(0xffffffffu, (p ? vs : ks)[32 * i / kPieces / 32], r & 31);
+        const uint32_t w[4] = {raw[p][i].x, raw[p][i].y, raw[p][i].z, raw[p][i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          float x[4];
+          b8::decode4(w[j], sc, x);
+          o[j] = b8::encode4(__fmul_rn(x[0], inv), __fmul_rn(x[1], inv), __fmul_rn(x[2], inv),
+                             __fmul_rn(x[3], inv));
+        }
+        if (has[32 * i / kPieces / 32] >> (r & 31) & 1)
+          *reinterpret_cast<uint4 *>(out + 16 * (lane + 32 * i)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      if (lane == 0 && run == 0) (p ? a.dst.v_scales : a.dst.k_scales)[dh] = scale;
     }
   }
-  if (threadIdx.x == 0) (is_v ? a.dst.v_scales : a.dst.k_scales)[dh] = scale;
 }
 
 }  // namespace
@@ -228,22 +313,27 @@ cudaError_t launch_b8_evict(const kvq_b8_cache &src, const kvq_b8_cache &dst, in
                             int64_t mass_out_stride, cudaStream_t s) {
   const EvictArgs a = {src,  dst,         batch,    max_seq_len, keep,     recent,          sinks, seq_lens,
                        mass, mass_stride, new_lens, kept,        mass_out, mass_out_stride, device_error_word()};
-  b8_select_kernel<<<batch * src.num_kv_heads, kSelThreads, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  // keys of up to 48 K tokens stay in shared memory between the passes
+  const int cached = min(max_seq_len, 49152);
+  cudaError_t e = cudaFuncSetAttribute(b8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       49152 * 4);
+  if (e != cudaSuccess) return e;
+  b8_select_kernel<<<batch * src.num_kv_heads, kSelThreads, cached * 4, s>>>(a, cached);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int cols = (min(keep, max_seq_len) + dst.block_size - 1) / dst.block_size;
   if (cols == 0) return cudaSuccess;
-  const int items = dst.block_size * (dst.head_dim / 16);
-  int threads = 32;
-  while (threads < 256 && threads < items) threads *= 2;
-  while (threads * kItems < items) threads *= 2;
-  const unsigned ctas = (unsigned)(2LL * cols * batch * src.num_kv_heads);
-  // blocks above 1024 pieces want up to 1024 threads, whose 64 registers each
-  // would spill: two instances
-  if (threads <= 256)
-    b8_requant_kernel<256><<<ctas, threads, 0, s>>>(a, cols);
-  else
-    b8_requant_kernel<1024><<<ctas, threads, 0, s>>>(a, cols);
+  const int64_t units = (int64_t)cols * batch * src.num_kv_heads;
+  const int runs = max(1, dst.block_size * dst.head_dim / 4096);
+  const int threads = runs > 1 ? 32 * runs : 128;
+  // 16 warps an SM hold 128 KB of codes
+  const int64_t resident = (int64_t)kNumSMs * max(1, 512 / threads);
+  const unsigned ctas = (unsigned)min(runs > 1 ? units : (units + 3) / 4, resident);
+  switch (dst.head_dim) {
+    case 64: b8_requant_kernel<64><<<ctas, threads, 0, s>>>(a, cols, runs, units); break;
+    case 128: b8_requant_kernel<128><<<ctas, threads, 0, s>>>(a, cols, runs, units); break;
+    default: b8_requant_kernel<256><<<ctas, threads, 0, s>>>(a, cols, runs, units); break;
+  }
   return cudaGetLastError();
 }
 

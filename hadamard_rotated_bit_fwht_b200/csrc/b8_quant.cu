@@ -4,9 +4,10 @@
 // Per (block, kv head) of K or V: scale = max(amax / 127, old), codes
 // rint(x / scale).  One CTA owns one block of one head, so the scale, the new
 // codes and the rescaled older codes have one writer and nothing depends on
-// an order.  The new rows are read once and kept in registers between the
-// maximum and the rounding; blocks too large for that (more than kItems
-// 16-element pieces a thread) are read a second time, from L2.
+// an order.  The new rows are read once; between the maximum and the rounding
+// their rotated fp32 values wait in shared memory (each thread reads back what
+// it wrote).  Blocks too large for that (more than kKeep bytes) are read and
+// rotated a second time.
 #include "b8_common.cuh"
 #include "rope.cuh"
 
@@ -16,11 +17,12 @@ namespace {
 using namespace rope;
 
 constexpr int kThreads = 256;
-constexpr int kItems = 4;  // pieces of 16 elements a thread keeps
+constexpr int kKeep = 64 * 1024;  // fp32 bytes of a block's new rows, three CTAs an SM
+constexpr int kAhead = 2;         // pieces whose loads are in flight together
 
 // grid: (touched block of the sequence + cols * (2 * sequence + is_v), kv head)
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads)
+template <bool BF16, bool KEEP>
+__global__ void __launch_bounds__(kThreads, 3)
     b8_append_kernel(kvq_b8_cache c, kvq_heads k, kvq_heads v, int t_new, int cols,
                      const int32_t *__restrict__ start_pos, const int32_t *__restrict__ new_lens,
                      kvq_rope_spec spec, const int32_t *__restrict__ rope_pos,
@@ -49,50 +51,71 @@ __global__ void __launch_bounds__(kThreads)
   const bool turned = !is_v && spec.d_inv_freq != nullptr;
   const int rot = turned ? spec.rot_dim : 0;
 
-  auto fetch = [&](int it, float (&x)[8], float (&y)[8], int &row, Piece &p) {
-    row = it / pieces;
-    p = piece(it - row * pieces, rot, spec.interleaved);
-    const int64_t tok = (int64_t)b * t_new + (lo - start) + row;
-    const int64_t at = tok * src.token_stride + h * src.head_stride;
-    Raw8<BF16> ra, rb;
-    load8<BF16>(src.data, at + p.a, ra);
-    load8<BF16>(src.data, at + p.b, rb);
+  // blockDim is a multiple of the pieces of a row: a thread's pieces are the
+  // same dims of different rows
+  const Piece p = piece(threadIdx.x & (pieces - 1), rot, spec.interleaved);
+  const int row_shift = __ffs(pieces) - 1;
+  uint64_t rate[8];
+  if (p.pair >= 0) {
+#pragma unroll
+    for (int e = 0; e < 8; e++) rate[e] = turn_rate(__ldg(spec.d_inv_freq + p.pair + e));
+  }
+  const int64_t tok0 = (int64_t)b * t_new + (lo - start);
+  auto turned_piece = [&](int row, const Raw8<BF16> &ra, const Raw8<BF16> &rb, float (&x)[8],
+                          float (&y)[8]) {
     widen8<BF16>(ra, x);
     widen8<BF16>(rb, y);
     if (p.pair >= 0) {
-      const int pos = rope_pos ? __ldg(rope_pos + tok) : (int)(lo + row);
+      const int pos = rope_pos ? __ldg(rope_pos + tok0 + row) : (int)(lo + row);
       float2 cs[8];
 #pragma unroll
-      for (int e = 0; e < 8; e++) cs[e] = turn(pos, __ldg(spec.d_inv_freq + p.pair + e), spec.factor);
+      for (int e = 0; e < 8; e++) cs[e] = turn(pos, rate[e], spec.factor);
       rotate_piece(x, y, cs, spec.interleaved);
     }
   };
-
-  const bool keep = items <= kItems * (int)blockDim.x;
-  float xs[kItems][8], ys[kItems][8];
-  float amax = 0.f;
-  if (keep) {
+  extern __shared__ float4 kept[];  // [piece of the thread][4][thread]
+  auto put = [&](const float (&x)[8], const float (&y)[8], int row, float inv) {
+    int8_t *at = codes + (int64_t)(r0 + row) * D;
+    *reinterpret_cast<uint2 *>(at + p.a) = b8::encode8(x, inv);
+    *reinterpret_cast<uint2 *>(at + p.b) = b8::encode8(y, inv);
+  };
+  // every piece of the thread, kAhead at a time: f(piece number, row, x, y)
+  auto each = [&](auto f) {
+    int n = 0;
+    for (int it = threadIdx.x; it < items; it += kAhead * blockDim.x, n += kAhead) {
+      Raw8<BF16> ra[kAhead], rb[kAhead];
 #pragma unroll
-    for (int i = 0; i < kItems; i++) {
-      const int it = threadIdx.x + i * blockDim.x;
-      if (it < items) {
-        int row;
-        Piece p;
-        fetch(it, xs[i], ys[i], row, p);
+      for (int k = 0; k < kAhead; k++) {
+        const int row = (it + k * (int)blockDim.x) >> row_shift;
+        if (it + k * (int)blockDim.x < items) {
+          const int64_t at = (tok0 + row) * src.token_stride + h * src.head_stride;
+          load8<BF16>(src.data, at + p.a, ra[k]);
+          load8<BF16>(src.data, at + p.b, rb[k]);
+        }
+      }
 #pragma unroll
-        for (int e = 0; e < 8; e++) amax = fmaxf(amax, fmaxf(fabsf(xs[i][e]), fabsf(ys[i][e])));
+      for (int k = 0; k < kAhead; k++) {
+        const int row = (it + k * (int)blockDim.x) >> row_shift;
+        if (it + k * (int)blockDim.x < items) {
+          float x[8], y[8];
+          turned_piece(row, ra[k], rb[k], x, y);
+          f(n + k, row, x, y);
+        }
       }
     }
-  } else {
-    for (int it = threadIdx.x; it < items; it += blockDim.x) {
-      int row;
-      Piece p;
-      float x[8], y[8];
-      fetch(it, x, y, row, p);
+  };
+  float amax = 0.f;
+  each([&](int n, int row, const float (&x)[8], const float (&y)[8]) {
 #pragma unroll
-      for (int e = 0; e < 8; e++) amax = fmaxf(amax, fmaxf(fabsf(x[e]), fabsf(y[e])));
+    for (int e = 0; e < 8; e++) amax = fmaxf(amax, fmaxf(fabsf(x[e]), fabsf(y[e])));
+    if (KEEP) {
+      float4 *at = kept + (size_t)n * 4 * blockDim.x + threadIdx.x;
+      at[0] = make_float4(x[0], x[1], x[2], x[3]);
+      at[blockDim.x] = make_float4(x[4], x[5], x[6], x[7]);
+      at[2 * blockDim.x] = make_float4(y[0], y[1], y[2], y[3]);
+      at[3 * blockDim.x] = make_float4(y[4], y[5], y[6], y[7]);
     }
-  }
+  });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
@@ -102,28 +125,17 @@ __global__ void __launch_bounds__(kThreads)
   const float scale = fmaxf(b8::scale_of(amax), old);
   const float inv = b8::inverse(scale);
 
-  auto put = [&](const float (&x)[8], const float (&y)[8], int row, const Piece &p) {
-    int8_t *at = codes + (int64_t)(r0 + row) * D;
-    *reinterpret_cast<uint2 *>(at + p.a) = b8::encode8(x, inv);
-    *reinterpret_cast<uint2 *>(at + p.b) = b8::encode8(y, inv);
-  };
-  if (keep) {
-#pragma unroll
-    for (int i = 0; i < kItems; i++) {
-      const int it = threadIdx.x + i * blockDim.x;
-      if (it < items) {
-        const int row = it / pieces;
-        put(xs[i], ys[i], row, piece(it - row * pieces, rot, spec.interleaved));
-      }
+  if (KEEP) {
+    int n = 0;
+    for (int it = threadIdx.x; it < items; it += blockDim.x, n++) {
+      const float4 *at = kept + (size_t)n * 4 * blockDim.x + threadIdx.x;
+      const float4 u0 = at[0], u1 = at[blockDim.x], v0 = at[2 * blockDim.x], v1 = at[3 * blockDim.x];
+      const float x[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+      const float y[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+      put(x, y, it >> row_shift, inv);
     }
   } else {
-    for (int it = threadIdx.x; it < items; it += blockDim.x) {
-      int row;
-      Piece p;
-      float x[8], y[8];
-      fetch(it, x, y, row, p);
-      put(x, y, row, p);
-    }
+    each([&](int, int row, const float (&x)[8], const float (&y)[8]) { put(x, y, row, inv); });
   }
   // the block's earlier rows follow a scale that grew
   if (old > 0.f && scale > old) {
@@ -139,47 +151,71 @@ __global__ void __launch_bounds__(kThreads)
   if (threadIdx.x == 0) *scale_at = scale;
 }
 
-// grid-stride over 16-element pieces of the output; adjacent threads take
-// adjacent 16-byte code chunks
-template <bool BF16>
+// grid: (run of kN x 256 pieces of a sequence's rows, sequence).  A piece is 8
+// elements of K and of V: adjacent threads store adjacent 16 (bf16) or 32
+// bytes, and all of a thread's codes and scales are on their way before the
+// first is used.
+template <bool BF16, int D, int kN>
 __global__ void __launch_bounds__(kThreads)
-    b8_gather_kernel(kvq_b8_cache c, int64_t total, int count,
+    b8_gather_kernel(kvq_b8_cache c, uint32_t total, int count,
                      const int32_t *__restrict__ first, const int32_t *__restrict__ ends,
                      void *__restrict__ k_out, void *__restrict__ v_out,
                      uint32_t *__restrict__ err) {
-  const int pieces = c.head_dim / 16;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = i / pieces;
-    const int j = (int)(i - row * pieces);
-    const int64_t bt = row / c.num_kv_heads;
-    const int h = (int)(row - bt * c.num_kv_heads);
-    const int b = (int)(bt / count);
-    const int64_t t = (int64_t)__ldg(first + b) + (bt - (int64_t)b * count);
-    int64_t slot = -1;
-    if (t >= 0 && t < __ldg(ends + b) && t < (int64_t)c.max_blocks_per_seq * c.block_size)
-      slot = b8::block_of(c, b, (int)(t / c.block_size));
-    if (slot >= 0 && !in_bounds(slot, slot + 1, c.num_blocks, err)) slot = -1;
-    const int64_t sh = slot * c.num_kv_heads + h;
-    const int64_t at = (sh * c.block_size + t % c.block_size) * c.head_dim + 16 * j;
-    const int64_t to = row * c.head_dim + 16 * j;
+  constexpr uint32_t kPieces = D / 8;
+  const int b = blockIdx.y;
+  const uint32_t hkv = c.num_kv_heads;
+  const int shift = __ffs(c.block_size) - 1;
+  const int64_t t0 = __ldg(first + b);
+  const int64_t cap = min((int64_t)__ldg(ends + b), (int64_t)c.max_blocks_per_seq * c.block_size);
+  uint2 kw[kN], vw[kN];
+  float ks[kN], vs[kN];
+  const uint32_t i0 = blockIdx.x * (kN * kThreads) + threadIdx.x;
 #pragma unroll
-    for (int w = 0; w < 2; w++) {
-      float x[8] = {}, y[8] = {};
-      if (slot >= 0) {
-        const uint4 u = *reinterpret_cast<const uint4 *>((w ? c.v_codes : c.k_codes) + at);
-        const float s = (w ? c.v_scales : c.k_scales)[sh];
-        b8::decode4(u.x, s, x), b8::decode4(u.y, s, x + 4);
-        b8::decode4(u.z, s, y), b8::decode4(u.w, s, y + 4);
-      }
-      void *out = w ? v_out : k_out;
-      store8<BF16>(out, to, x);
-      store8<BF16>(out, to + 8, y);
-    }
+  for (int n = 0; n < kN; n++) {
+    const uint32_t i = i0 + n * kThreads;
+    kw[n] = vw[n] = make_uint2(0, 0);
+    ks[n] = vs[n] = 0.f;
+    const uint32_t row = i / kPieces, tok = row / hkv, h = row - tok * hkv;
+    const int64_t t = t0 + tok;
+    int64_t slot = -1;
+    if (i < total && t >= 0 && t < cap) slot = b8::block_of(c, b, (int)(t >> shift));
+    if (slot < 0 || !in_bounds(slot, slot + 1, c.num_blocks, err)) continue;
+    const int64_t sh = slot * hkv + h;
+    const int64_t at = ((sh << shift) + (t & (c.block_size - 1))) * D + 8 * (i % kPieces);
+    kw[n] = __ldg(reinterpret_cast<const uint2 *>(c.k_codes + at));
+    vw[n] = __ldg(reinterpret_cast<const uint2 *>(c.v_codes + at));
+    ks[n] = __ldg(c.k_scales + sh);
+    vs[n] = __ldg(c.v_scales + sh);
+  }
+#pragma unroll
+  for (int n = 0; n < kN; n++) {
+    const uint32_t i = i0 + n * kThreads;
+    if (i >= total) break;
+    const int64_t to = ((int64_t)b * total + i) * 8;
+    float x[8];
+    b8::decode4(kw[n].x, ks[n], x), b8::decode4(kw[n].y, ks[n], x + 4);
+    store8<BF16>(k_out, to, x);
+    b8::decode4(vw[n].x, vs[n], x), b8::decode4(vw[n].y, vs[n], x + 4);
+    store8<BF16>(v_out, to, x);
   }
 }
 
 }  // namespace
+
+template <bool BF16, bool KEEP>
+static cudaError_t append(const kvq_b8_cache &c, const kvq_heads &k, const kvq_heads &v, dim3 grid,
+                          int threads, int smem, int cols, int t_new,
+                          const int32_t *start_pos, const int32_t *new_lens,
+                          const kvq_rope_spec &spec, const int32_t *rope_pos, cudaStream_t s) {
+  auto *f = b8_append_kernel<BF16, KEEP>;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeep);
+    if (e != cudaSuccess) return e;
+  }
+  f<<<grid, threads, smem, s>>>(c, k, v, t_new, cols, start_pos, new_lens, spec, rope_pos,
+                                device_error_word());
+  return cudaGetLastError();
+}
 
 cudaError_t launch_b8_append(const kvq_b8_cache &c, const kvq_heads &k, const kvq_heads &v,
                              int bf16, int batch, int t_new, const int32_t *start_pos,
@@ -190,27 +226,39 @@ cudaError_t launch_b8_append(const kvq_b8_cache &c, const kvq_heads &k, const kv
   int threads = 32;
   while (threads < kThreads && threads < items) threads *= 2;
   const dim3 grid((unsigned)cols * 2u * batch, c.num_kv_heads);
+  // 64 bytes a piece, whole rounds of the threads
+  const int64_t bytes = (int64_t)(items + threads - 1) / threads * threads * 64;
+  const bool keep = bytes <= kKeep;
+  auto *f = bf16 ? (keep ? append<true, true> : append<true, false>)
+                 : (keep ? append<false, true> : append<false, false>);
+  return f(c, k, v, grid, threads, keep ? (int)bytes : 0, cols, t_new, start_pos, new_lens, spec,
+           rope_pos, s);
+}
+
+template <bool BF16, int D>
+static void gather(const kvq_b8_cache &c, int batch, const int32_t *first, const int32_t *ends,
+                   int count, void *k_out, void *v_out, cudaStream_t s) {
   uint32_t *err = device_error_word();
-  if (bf16)
-    b8_append_kernel<true><<<grid, threads, 0, s>>>(c, k, v, t_new, cols, start_pos, new_lens, spec,
-                                                    rope_pos, err);
-  else
-    b8_append_kernel<false><<<grid, threads, 0, s>>>(c, k, v, t_new, cols, start_pos, new_lens, spec,
-                                                     rope_pos, err);
-  return cudaGetLastError();
+  const uint32_t total = (uint32_t)count * c.num_kv_heads * (D / 8);
+  // four pieces a thread once one a thread would fill the card
+  if ((int64_t)total * batch > (int64_t)kNumSMs * 2048) {
+    const dim3 grid((total + 4 * kThreads - 1) / (4 * kThreads), batch);
+    b8_gather_kernel<BF16, D, 4>
+        <<<grid, kThreads, 0, s>>>(c, total, count, first, ends, k_out, v_out, err);
+  } else {
+    const dim3 grid((total + kThreads - 1) / kThreads, batch);
+    b8_gather_kernel<BF16, D, 1>
+        <<<grid, kThreads, 0, s>>>(c, total, count, first, ends, k_out, v_out, err);
+  }
 }
 
 cudaError_t launch_b8_gather(const kvq_b8_cache &c, int batch, const int32_t *first,
                              const int32_t *ends, int count, int bf16, void *k_out, void *v_out,
                              cudaStream_t s) {
-  const int64_t total = (int64_t)batch * count * c.num_kv_heads * (c.head_dim / 16);
-  const int64_t want = (total + kThreads - 1) / kThreads;
-  const int ctas = (int)min(want, (int64_t)kNumSMs * 8);
-  uint32_t *err = device_error_word();
-  if (bf16)
-    b8_gather_kernel<true><<<ctas, kThreads, 0, s>>>(c, total, count, first, ends, k_out, v_out, err);
-  else
-    b8_gather_kernel<false><<<ctas, kThreads, 0, s>>>(c, total, count, first, ends, k_out, v_out, err);
+  auto *f = c.head_dim == 64    ? (bf16 ? gather<true, 64> : gather<false, 64>)
+            : c.head_dim == 128 ? (bf16 ? gather<true, 128> : gather<false, 128>)
+                                : (bf16 ? gather<true, 256> : gather<false, 256>);
+  f(c, batch, first, ends, count, k_out, v_out, s);
   return cudaGetLastError();
 }
 

@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(kThreads)
   const float sign = inverse ? -1.f : 1.f;
   for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
     const int t = i / pairs, p = i - t * pairs;
-    float2 c = turn(__ldg(positions + t0 + t), __ldg(spec.d_inv_freq + p), spec.factor);
+    float2 c = turn(__ldg(positions + t0 + t), turn_rate(__ldg(spec.d_inv_freq + p)), spec.factor);
     c.y *= sign;
     cs[i] = c;
   }

@@ -10,17 +10,22 @@
 namespace kvq {
 namespace rope {
 
-// cos t and sin t of t = pos * w radians, times factor.  The angle is formed
-// in half turns in fp64 and reduced to [-1, 1] there (positions reach 2^31 and
-// pos * w / pi keeps 53 bits, so what is left has an error below 2^-20 of a
-// half turn even at pos * w = 2^32, and 2^-36 below 2^16); its rounding to
-// fp32 moves the angle by at most 2^-25 half turns, 9.4e-8 radians, which is
-// the size of fp32's own rounding of the products that follow.
-__device__ __forceinline__ float2 turn(int pos, double w, float factor) {
-  const double h = (double)pos * w * 0.31830988618379067154;
-  const float r = (float)(h - 2.0 * rint(0.5 * h));
+// Angles are counted in 2^-64 turns, modulo one turn: an integer product with
+// the position wraps exactly, however far the position.  turn_rate turns
+// radians per position into that unit (fp64: w / 2 pi has a relative error of
+// 2^-52, so the angle is off by 2^-52 of the turns made).
+__device__ __forceinline__ uint64_t turn_rate(double w) {
+  const double f = w * 0.15915494309189533577;
+  return (uint64_t)__double2ll_rn((f - rint(f)) * 0x1p63) << 1;
+}
+// cos t and sin t, times factor.  The leading 32 bits of the angle become
+// half turns in [-1, 1) in fp32, whose rounding moves the angle by at most
+// 2^-25 half turns, 9.4e-8 radians: the size of fp32's own rounding of the
+// products that follow.
+__device__ __forceinline__ float2 turn(int pos, uint64_t rate, float factor) {
+  const int hi = (int)((rate * (uint64_t)(int64_t)pos) >> 32);
   float s, c;
-  sincospif(r, &s, &c);
+  sincospif((float)hi * 0x1p-31f, &s, &c);
   return make_float2(c * factor, s * factor);
 }
 
