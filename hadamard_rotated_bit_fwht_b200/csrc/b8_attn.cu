@@ -30,6 +30,7 @@ constexpr float kEmpty = -1e30f;  // running maximum before any token
 constexpr float kSlack = 8.f;
 constexpr int64_t kPrefillRows = 64;
 
+// HILO: fp32 output, probabilities as fp16 hi + lo
 template <int D, int R, bool HILO>
 struct Cfg {
   static constexpr int kTileBytes = kTok * D;           // K or V of a warp's tile
@@ -40,7 +41,7 @@ struct Cfg {
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   // after the ring: queries, their factors and their token limits
   static constexpr int kOffQ = kRing;
-  static constexpr int kOffInv = kOffQ + QTile<D, R, HILO>::kBytes;
+  static constexpr int kOffInv = kOffQ + QTile<D, R>::kBytes;
   static constexpr int kOffLim = kOffInv + R * 4;
   static constexpr int kSmem = kOffLim + R * 4;
   // the merge reuses the ring: per warp R x (D + 4) of O, then m, l and vref
@@ -70,8 +71,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
   using C = Cfg<D, R, HILO>;
   constexpr int kNb = R / 8;       // n blocks of the second product
   constexpr int kMt = D / 16;      // m tiles of the second product
-  constexpr int kKs = D / 16;      // k steps of the first product
-  constexpr int kL = QTile<D, R, HILO>::kLevels;
+  constexpr int kKs = D / 32;      // k steps of the first product
+  constexpr int kL = QTile<D, R>::kLevels;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, tg = lane & 3;
@@ -105,19 +106,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
   const int first = t0 / kTok + warp;
   const int n_tiles = t1 > t0 ? max(0, ((t1 + kTok - 1) / kTok - first + kWarps - 1) / kWarps) : 0;
   uint8_t *ring = smem + warp * C::kStages * C::kStageBytes;
-  const int per_block = c.block_size / kTok;
+  const int per_block = c.block_size / kTok, pb_shift = __ffs(per_block) - 1;
   const int32_t *table = c.block_table + (int64_t)b * c.max_blocks_per_seq;
   // lane l holds the block of tile page_base + l
   int page_base = 0, page = -1;
   auto load_pages = [&](int base) {
     page_base = base;
-    const int col = (first + (base + lane) * kWarps) / per_block;
+    const int col = (first + (base + lane) * kWarps) >> pb_shift;
     page = base + lane < n_tiles && col < c.max_blocks_per_seq ? __ldg(table + col) : -1;
     if (page >= c.num_blocks) page = -1;
   };
   uint32_t live = 0;  // bit s: the tile in stage s is mapped
-  auto issue = [&](int it) {
-    const int st = it % C::kStages;
+  // 16-byte chunk lane + 32 i of a tile is chunk kc of row kr + i * kStep
+  constexpr int kStep = 512 / D;
+  const int kr = lane / (D / 16), kc = lane % (D / 16);
+  auto issue = [&](int it, int st) {
     if (it < n_tiles) {
       if (it >= page_base + 32) load_pages(it);
       const int slot = __shfl_sync(0xffffffffu, page, it - page_base);
@@ -126,13 +129,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
       live = mapped ? live | (1u << st) : live & ~(1u << st);
       if (mapped) {
         const int64_t sh = (int64_t)slot * c.num_kv_heads + kvh;
-        const int64_t off = (sh * c.block_size + tile % per_block * kTok) * D;
+        const int64_t off = (sh * c.block_size + (tile & (per_block - 1)) * kTok) * D + 16 * lane;
         const uint32_t dst = smem_u32(ring + st * C::kStageBytes);
+        const int8_t *ksrc = c.k_codes + off, *vsrc = c.v_codes + off;
 #pragma unroll
         for (int i = 0; i < C::kTileBytes / 512; i++) {
-          const int ch = lane + 32 * i, r = ch / (D / 16), cc = ch % (D / 16);
-          cp_async16(dst + k_off<D>(r, cc), c.k_codes + off + 16 * ch);
-          cp_async16(dst + C::kTileBytes + v_off<D>(r, cc), c.v_codes + off + 16 * ch);
+          cp_async16(dst + k_off<D>(kr + i * kStep, kc), ksrc + 512 * i);
+          cp_async16(dst + C::kTileBytes + v_off<D>(kr + i * kStep, kc), vsrc + 512 * i);
         }
         if (lane < 2)
           cp_async4(dst + 2 * C::kTileBytes + 4 * lane, (lane ? c.v_scales : c.k_scales) + sh);
@@ -142,9 +145,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
   };
   if (n_tiles > 0) load_pages(0);
 #pragma unroll
-  for (int i = 0; i < C::kStages - 1; i++) issue(i);
+  for (int i = 0; i < C::kStages - 1; i++) issue(i, i);
 
-  stage_queries<D, R, HILO>(a.q, q0, kvh, row0, n_rows, warp, kWarps, lane, qimg, inv_s);
+  stage_queries<D, R, !HILO>(a.q, q0, kvh, row0, n_rows, warp, kWarps, lane, qimg, inv_s);
   if (tid < R) lim_s[tid] = row0 + tid < n_rows ? max(0, len - nq + (row0 + tid) / a.q.group + 1) : 0;
   __syncthreads();
   const float inv0 = inv_s[g], inv1 = R == 16 ? inv_s[R == 16 ? g + 8 : g] : 0.f;
@@ -152,11 +155,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
   const bool whole = row0 + R <= n_rows;
 
   constexpr bool kQRegs = R == 8 && D <= 128;
-  uint4 qr[kQRegs ? kKs : 1];
+  uint4 qr[kQRegs ? kKs * kL : 1];
   if (kQRegs) {
 #pragma unroll
-    for (int ks = 0; ks < kKs; ks++)
-      qr[kQRegs ? ks : 0] = *reinterpret_cast<const uint4 *>(qimg + (ks * 32 + lane) * 4);
+    for (int i = 0; i < kKs * kL; i++)
+      qr[kQRegs ? i : 0] = *reinterpret_cast<const uint4 *>(qimg + (i * 32 + lane) * 4);
   }
 
   float o[kMt][kNb][4];
@@ -169,26 +172,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
   float m[kNb], l[kNb];
 #pragma unroll
   for (int n = 0; n < kNb; n++) m[n] = kEmpty, l[n] = 0.f;
-  float vref = 0x1p-100f;
+  float vref = 0x1p-100f, vinv = 0x1p106f;  // vinv: 64 / vref
+  // rows of the V matrices that this lane addresses
+  const int v_row = (lane & 7) + (lane & 8), v_ch = lane >> 4;
 
-  for (int it = 0; it < n_tiles; it++) {
+  for (int it = 0, st = 0; it < n_tiles; it++, st = st + 1 == C::kStages ? 0 : st + 1) {
     cp_wait<C::kStages - 2>();
     __syncwarp();
-    issue(it + C::kStages - 1);
-    const int st = it % C::kStages;
+    issue(it + C::kStages - 1, st == 0 ? C::kStages - 1 : st - 1);
     if (!(live >> st & 1)) continue;
-    const uint8_t *kt = ring + st * C::kStageBytes, *vt = kt + C::kTileBytes;
-    const float ks_ = *reinterpret_cast<const float *>(kt + 2 * C::kTileBytes);
-    const float vs_ = *reinterpret_cast<const float *>(kt + 2 * C::kTileBytes + 4);
+    const uint8_t *kt = ring + st * C::kStageBytes;
+    const uint32_t vt = smem_u32(kt + C::kTileBytes);
+    const float2 kv = *reinterpret_cast<const float2 *>(kt + 2 * C::kTileBytes);  // scales
     const int tok = (first + it * kWarps) * kTok;
 
-    // S: rows g (c0, c1) and g + 8 (c2, c3), tokens 8 n + 2 tg, + 1
-    float s[2][4];
+    // S: rows g (0, 1) and g + 8 (2, 3), tokens 8 n + 2 tg, + 1, of each level
+    uint32_t s[2][kL][4];
 #pragma unroll
-    for (int n = 0; n < 2; n++) {
+    for (int n = 0; n < 2; n++)
 #pragma unroll
-      for (int e = 0; e < 4; e++) s[n][e] = 0.f;
-    }
+      for (int v = 0; v < kL; v++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) s[n][v][e] = kMagicBits;
 #pragma unroll
     for (int blk = 0; blk < D / 64; blk++) {
       uint4 kw[2];
@@ -196,38 +201,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
       for (int n = 0; n < 2; n++)
         kw[n] = *reinterpret_cast<const uint4 *>(kt + k_off<D>(8 * n + g, 4 * blk + tg));
 #pragma unroll
-      for (int w = 0; w < 4; w++) {
-        const int ks = 4 * blk + w;
-        uint4 qa[kL];
-        if (kQRegs) {
-          qa[0] = qr[kQRegs ? ks : 0];
-        } else {
+      for (int h = 0; h < 2; h++) {
+        const int ks = 2 * blk + h;
 #pragma unroll
-          for (int v = 0; v < kL; v++)
-            qa[v] = *reinterpret_cast<const uint4 *>(qimg + ((ks * kL + v) * 32 + lane) * 4);
-        }
+        for (int v = 0; v < kL; v++) {
+          const uint4 qa = kQRegs ? qr[kQRegs ? ks * kL + v : 0]
+                                  : *reinterpret_cast<const uint4 *>(qimg + ((ks * kL + v) * 32 + lane) * 4);
 #pragma unroll
-        for (int n = 0; n < 2; n++) {
-          uint32_t b0, b1;
-          k_frag(word(kw[n], w), b0, b1);
-#pragma unroll
-          for (int v = 0; v < kL; v++) mma16816(s[n], qa[v], b0, b1);
+          for (int n = 0; n < 2; n++)
+            imma(s[n][v], qa, h ? kw[n].z : kw[n].x, h ? kw[n].w : kw[n].y);
         }
       }
     }
     // scores in log2 units, p[row block][token pair]
     float p[kNb][4];
-    float tmax[kNb];
 #pragma unroll
     for (int nb = 0; nb < kNb; nb++) {
-      const float f = __fmul_rn(nb ? inv1 : inv0, ks_);
+      const float f = (nb ? inv1 : inv0) * kv.x;
 #pragma unroll
       for (int n = 0; n < 2; n++)
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-          float x = s[n][2 * nb + e];
-          if (R == 8 && HILO) x += s[n][2 + e];
-          p[nb][2 * n + e] = x * f;
+          const float hi = isum(s[n][0][2 * nb + e]);
+          const float mid = isum(R == 8 ? s[n][0][2 + e] : s[n][1][2 * nb + e]);
+          const float lo = isum(R == 8 ? s[n][1][e] : s[n][kL - 1][2 * nb + e]);
+          p[nb][2 * n + e] = fmaf(hi, 16384.f, fmaf(mid, 128.f, lo)) * f;
         }
     }
     if (tok + kTok > lo_lim || !whole) {
@@ -237,28 +235,27 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
         for (int e = 0; e < 4; e++)
           if (tok + 8 * (e >> 1) + 2 * tg + (e & 1) >= (nb ? lim1 : lim0)) p[nb][e] = -INFINITY;
     }
-    bool grow = false;
-    const bool vgrow = vs_ > vref;
+    // m need not be the maximum: it moves once a score passes it by kSlack
+    const bool vgrow = kv.y > vref;
+    bool grow = vgrow;
 #pragma unroll
-    for (int nb = 0; nb < kNb; nb++) {
-      float x = fmaxf(fmaxf(p[nb][0], p[nb][1]), fmaxf(p[nb][2], p[nb][3]));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-      tmax[nb] = x;
-      grow |= x > m[nb] + kSlack;
-    }
-    if (__any_sync(0xffffffffu, grow) || vgrow) {
+    for (int nb = 0; nb < kNb; nb++)
+      grow |= fmaxf(fmaxf(p[nb][0], p[nb][1]), fmaxf(p[nb][2], p[nb][3])) > m[nb] + kSlack;
+    if (__any_sync(0xffffffffu, grow)) {
       float vfac = 1.f;
       if (vgrow) {
         // power of two at or above the scale (infinite scales give NaN)
-        const uint32_t ex = (__float_as_uint(vs_) + 0x7fffffu) & 0x7f800000u;
-        const float nref = __uint_as_float(ex);
+        const float nref = __uint_as_float((__float_as_uint(kv.y) + 0x7fffffu) & 0x7f800000u);
         vfac = __fdiv_rn(vref, nref);
         vref = nref;
+        vinv = __fdiv_rn(64.f, nref);
       }
 #pragma unroll
       for (int nb = 0; nb < kNb; nb++) {
-        const float mn = tmax[nb] > m[nb] + kSlack ? tmax[nb] : m[nb];
+        float x = fmaxf(fmaxf(p[nb][0], p[nb][1]), fmaxf(p[nb][2], p[nb][3]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        const float mn = x > m[nb] + kSlack ? x : m[nb];
         const float al = ex2(m[nb] - mn);
         l[nb] *= al;
         m[nb] = mn;
@@ -272,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
         }
       }
     }
-    const float vf = __fdiv_rn(vs_ * 64.f, vref);
+    const float vf = kv.y * vinv;
     uint32_t ph[kNb][2], pl[kNb][2];
 #pragma unroll
     for (int nb = 0; nb < kNb; nb++) {
@@ -287,39 +284,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
           ph[nb][n] = pack_f16x2(w.x, w.y);
       }
     }
-    // O^T += V^T P^T.  The k index 2 tg + {0, 1} of the fragments is token
-    // 2 tg + {0, 1}, 2 tg + 8 + {0, 1} token 8 + 2 tg + {0, 1}.
-    constexpr int kPieces = D == 64 ? 1 : D / 128;  // 16 (8) dims of each token
+    // O^T += V^T P^T, two m tiles a load
 #pragma unroll
-    for (int pc = 0; pc < kPieces; pc++) {
-      uint4 vw[4];
+    for (int j = 0; j < kMt; j += 2) {
+      uint32_t w[4];  // tokens 0 .. 7 and 8 .. 15 of chunk j, then of chunk j + 1
+      dec::ldsm_x4_t(vt + v_off<D>(v_row, j + v_ch), w);
 #pragma unroll
-      for (int t = 0; t < 4; t++) {
-        const int r = 2 * tg + (t & 1) + 8 * (t >> 1);
-        if (D == 64) {
-          const uint2 x = *reinterpret_cast<const uint2 *>(vt + v_off<D>(r, g >> 1) + 8 * (g & 1));
-          vw[t] = make_uint4(x.x, x.y, 0, 0);
-        } else {
-          vw[t] = *reinterpret_cast<const uint4 *>(vt + v_off<D>(r, g + 8 * pc));
-        }
-      }
+      for (int h = 0; h < 2; h++) {
+        const uint32_t x = w[2 * h] ^ 0x80808080u, y = w[2 * h + 1] ^ 0x80808080u;
+        const uint32_t fr[4] = {pair_h2(x, 0x4240), pair_h2(x, 0x4341), pair_h2(y, 0x4240),
+                                pair_h2(y, 0x4341)};
 #pragma unroll
-      for (int w = 0; w < (D == 64 ? 2 : 4); w++) {
-        uint32_t f[4];
-#pragma unroll
-        for (int t = 0; t < 4; t++) f[t] = word(vw[t], w) ^ 0x80808080u;
-#pragma unroll
-        for (int h = 0; h < 2; h++) {  // dims 4 w + 2 h, + 1 of the piece
-          const uint32_t x = __byte_perm(f[0], f[1], h ? 0x7362 : 0x5140);
-          const uint32_t y = __byte_perm(f[2], f[3], h ? 0x7362 : 0x5140);
-          const uint32_t fr[4] = {pair_h2(x, 0x4140), pair_h2(x, 0x4342), pair_h2(y, 0x4140),
-                                  pair_h2(y, 0x4342)};
-          const int j = (D == 64 ? 0 : 8 * pc) + 2 * w + h;
-#pragma unroll
-          for (int nb = 0; nb < kNb; nb++) {
-            mma16816(o[j][nb], fr, ph[nb][0], ph[nb][1]);
-            if (HILO) mma16816(o[j][nb], fr, pl[nb][0], pl[nb][1]);
-          }
+        for (int nb = 0; nb < kNb; nb++) {
+          mma16816(o[j + h][nb], fr, ph[nb][0], ph[nb][1]);
+          if (HILO) mma16816(o[j + h][nb], fr, pl[nb][0], pl[nb][1]);
         }
       }
     }
@@ -342,11 +320,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
     for (int e = 0; e < 2; e++) {
       float *row = mo + (8 * nb + 2 * tg + e) * C::kRow;
 #pragma unroll
-      for (int j = 0; j < kMt; j += 2) {
-        const int d = D == 64 ? 8 * g + 2 * j : 128 * (j >> 3) + 16 * g + 2 * (j & 7);
-        *reinterpret_cast<float4 *>(row + d) =
-            make_float4(o[j][nb][e], o[j][nb][2 + e], o[j + 1][nb][e], o[j + 1][nb][2 + e]);
-      }
+      for (int j = 0; j < kMt; j++)
+        *reinterpret_cast<float2 *>(row + 16 * j + 2 * g) = make_float2(o[j][nb][e], o[j][nb][2 + e]);
     }
     if (tg == 0) {
       mm[warp * R + 8 * nb + g] = m[nb];
@@ -399,8 +374,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
 
 // One CTA per row: merge its splits' records.
 // grid: row of the tile + R * (row tile + row_tiles * (kv head + heads * sequence))
-constexpr int kCombine = 128;
-template <int D, bool HILO>
+template <int D, bool HILO, int kCombine>
 __global__ void __launch_bounds__(kCombine) b8_combine_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int kCols = D / 4, kParts = kCombine / kCols;
   __shared__ float part[kParts > 1 ? (kParts - 1) * D : 1];
@@ -475,7 +449,7 @@ cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int D, bool HILO>
+template <int D, bool HILO, int kCombine>
 cudaError_t combine(const AttnArgs &a, cudaStream_t s) {
   const int64_t units = (int64_t)a.q.batch * a.c.num_kv_heads * a.p.row_tiles;
   cudaLaunchConfig_t cfg = {};
@@ -487,7 +461,7 @@ cudaError_t combine(const AttnArgs &a, cudaStream_t s) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, b8_combine_kernel<D, HILO>, a);
+  return cudaLaunchKernelEx(&cfg, b8_combine_kernel<D, HILO, kCombine>, a);
 }
 
 template <int D>
@@ -500,7 +474,9 @@ cudaError_t by_rows(const AttnArgs &a, cudaStream_t s) {
   else
     e = a.q.bf16 ? launch<D, 16, false>(a, s) : launch<D, 16, true>(a, s);
   if (e != cudaSuccess || a.p.splits == 1) return e;
-  return a.q.bf16 ? combine<D, false>(a, s) : combine<D, true>(a, s);
+  // few rows of many splits want more threads a row
+  if (a.p.splits > 8) return a.q.bf16 ? combine<D, false, 512>(a, s) : combine<D, true, 512>(a, s);
+  return a.q.bf16 ? combine<D, false, 128>(a, s) : combine<D, true, 128>(a, s);
 }
 
 
@@ -523,12 +499,17 @@ B8Plan plan_b8_attn(const kvq_b8_cache &c, int bf16, int group, int batch, int m
     granule = b8_prefill_tokens(c.head_dim);
     want = min((int64_t)2 * kNumSMs / units, (len + 4 * granule - 1) / (4 * granule));
   } else {
-    // about four CTAs for each that the card holds at once, of at least 16 tiles
-    // a warp where that leaves one CTA for each
     const int resident = kNumSMs * (c.head_dim == 256 || p.rows == 16 ? 1 : 2);
     const int64_t full = (resident + units - 1) / units;  // splits that fill the card once
     granule = kWarps * kTok;
-    want = min((4 * (int64_t)resident + units - 1) / units, max(full, (len + 2047) / 2048));
+    if (batch == 1) {
+      // one length: whole waves of equal splits, as few as fill the card
+      want = max((int64_t)1, resident / units);
+    } else {
+      // lengths differ: about four CTAs for each that the card holds at once, of
+      // at least 16 tiles a warp where that leaves one CTA for each
+      want = min((4 * (int64_t)resident + units - 1) / units, max(full, (len + 2047) / 2048));
+    }
   }
   want = max((int64_t)1, min(want, (len + granule - 1) / granule));
   int64_t tokens = (len + want - 1) / want;

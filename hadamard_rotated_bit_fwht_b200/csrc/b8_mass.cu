@@ -3,11 +3,11 @@
 // group) that attend to token t of exp(score - lse).
 //
 // One CTA takes a range of tokens of a (sequence, kv head); a warp takes
-// kTiles 16-token tiles at a time, converts their K codes to fp16 fragments
-// once and runs every row over them, so each token has one owner: no atomics,
-// and the sum's order depends on the sizes alone.  Rows come in chunks staged
-// in shared memory (once if one chunk holds them all).  Bound for a few rows:
-// the K codes from HBM.
+// kTiles 16-token tiles at a time and runs every row over them, so each token
+// has one owner: no atomics, and the sum's order depends on the sizes alone.
+// Rows come in chunks of up to kChunk staged in shared memory; every chunk
+// walks the CTA's tokens, which then come from L2.  Bound for a few rows: the K
+// codes from HBM.
 #include "b8_mma.cuh"
 
 namespace kvq {
@@ -18,21 +18,20 @@ using namespace b8;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 
-template <int D, bool HILO>
+template <int D, int R>
 struct Cfg {
   static constexpr int kTiles = D == 256 ? 1 : 2;   // 16-token tiles of a warp's step
   static constexpr int kTileBytes = kTok * D;
   static constexpr int kStageBytes = kTiles * (kTileBytes + 16);  // + k_scale
-  static constexpr int kStages = 2;  // 64 KB in flight per SM
-  static constexpr int kChunk = 64;  // rows staged at once
-  using Q = QTile<D, 16, HILO>;
-  static constexpr int kOffQ = kWarps * kStages * kStageBytes;
-  static constexpr int kOffInv = kOffQ + kChunk / 16 * Q::kBytes;
+  static constexpr int kStages = 3;  // 128 KB in flight or landing per SM
+  static constexpr int kChunk = R == 8 ? 8 : 128;   // rows staged at once
+  using Q = QTile<D, R>;
+  static constexpr int kOffInv = kWarps * kStages * kStageBytes;
   static constexpr int kOffLse = kOffInv + kChunk * 4;
   static constexpr int kOffLim = kOffLse + kChunk * 4;
-  static constexpr int kSmem = kOffLim + kChunk * 4;
-  static constexpr int kCtas = D == 256 && HILO ? 1 : 2;
-  static_assert((kSmem + 1024) * kCtas <= 228 * 1024, "shared memory per SM");
+  static constexpr int kOffQ = kOffLim + kChunk * 4;  // last: as many row tiles as there are
+  static constexpr int smem(int row_tiles) { return kOffQ + row_tiles * Q::kBytes; }
+  static_assert(smem(kChunk / R) <= 227 * 1024, "shared memory per CTA");
 };
 
 struct MassArgs {
@@ -46,11 +45,11 @@ struct MassArgs {
 };
 
 // grid: range + ranges * (kv head + heads * sequence)
-template <int D, bool HILO>
-__global__ void __launch_bounds__(kThreads, Cfg<D, HILO>::kCtas)
+template <int D, int R, bool BF16>
+__global__ void __launch_bounds__(kThreads, 2)
     b8_mass_kernel(const __grid_constant__ MassArgs a) {
-  using C = Cfg<D, HILO>;
-  constexpr int kKs = D / 16, kL = C::Q::kLevels, kT = C::kTiles;
+  using C = Cfg<D, R>;
+  constexpr int kKs = D / 32, kL = C::Q::kLevels, kT = C::kTiles;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, tg = lane & 3;
@@ -72,10 +71,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, HILO>::kCtas)
   int *lim_s = reinterpret_cast<int *>(smem + C::kOffLim);
 
   // step it of this warp: tiles first + it * 8 * kT + {0 .. kT - 1}
-  const int first = t0 / kTok + warp * kT, end = (t1 + kTok - 1) / kTok;
-  const int n_steps = (end - t0 / kTok + kWarps * kT - 1) / (kWarps * kT);  // of the CTA
+  const int first = t0 / kTok + warp * kT;
+  int end = 0, n_steps = 0;  // of the chunk at hand
   uint8_t *ring = smem + warp * C::kStages * C::kStageBytes;
-  const int per_block = c.block_size / kTok;
+  const int per_block = c.block_size / kTok, pb_shift = __ffs(per_block) - 1;
   const int32_t *table = c.block_table + (int64_t)b * c.max_blocks_per_seq;
   int page_base = 0, page[kT];
   auto load_pages = [&](int base) {
@@ -83,13 +82,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, HILO>::kCtas)
 #pragma unroll
     for (int k = 0; k < kT; k++) {
       const int tile = first + (base + lane) * kWarps * kT + k;
-      page[k] = tile < end ? __ldg(table + tile / per_block) : -1;
+      page[k] = tile < end ? __ldg(table + (tile >> pb_shift)) : -1;
       if (page[k] >= c.num_blocks) page[k] = -1;
     }
   };
   uint32_t live = 0;  // bit kT * stage + k
-  auto issue = [&](int it) {
-    const int st = it % C::kStages;
+  constexpr int kStep = 512 / D;  // rows that a warp's 16-byte chunks cover
+  const int kr = lane / (D / 16), kc = lane % (D / 16);
+  auto issue = [&](int it, int st) {
     if (it < n_steps) {
       if (it >= page_base + 32) load_pages(it);
 #pragma unroll
@@ -101,31 +101,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, HILO>::kCtas)
         live = mapped ? live | bit : live & ~bit;
         if (mapped) {
           const int64_t sh = (int64_t)slot * c.num_kv_heads + kvh;
-          const int8_t *src = c.k_codes + (sh * c.block_size + tile % per_block * kTok) * D;
+          const int8_t *src = c.k_codes + (sh * c.block_size + (tile & (per_block - 1)) * kTok) * D + 16 * lane;
           const uint32_t dst =
               smem_u32(ring + st * C::kStageBytes + k * (C::kTileBytes + 16));
 #pragma unroll
-          for (int i = 0; i < C::kTileBytes / 512; i++) {
-            const int ch = lane + 32 * i;
-            cp_async16(dst + k_off<D>(ch / (D / 16), ch % (D / 16)), src + 16 * ch);
-          }
+          for (int i = 0; i < C::kTileBytes / 512; i++)
+            cp_async16(dst + k_off<D>(kr + i * kStep, kc), src + 512 * i);
           if (lane == 0) cp_async4(dst + C::kTileBytes, c.k_scales + sh);
         }
       }
     }
     cp_commit();
   };
-  load_pages(0);
-#pragma unroll
-  for (int i = 0; i < C::kStages - 1; i++) issue(i);
-
   const int n_chunks = (n_rows + C::kChunk - 1) / C::kChunk;
   auto stage_chunk = [&](int row0) {
-    const int tiles = (min(C::kChunk, n_rows - row0) + 15) / 16;
+    const int tiles = (min(C::kChunk, n_rows - row0) + R - 1) / R;
     for (int t = 0; t < tiles; t++)
-      stage_queries<D, 16, HILO>(a.q, q0, kvh, row0 + 16 * t, n_rows, warp, kWarps, lane,
-                                 qimg + t * C::Q::kWords, inv_s + 16 * t);
-    for (int r = tid; r < 16 * tiles; r += kThreads) {
+      stage_queries<D, R, BF16>(a.q, q0, kvh, row0 + R * t, n_rows, warp, kWarps, lane,
+                                qimg + t * C::Q::kWords, inv_s + R * t);
+    for (int r = tid; r < R * tiles; r += kThreads) {
       const int row = row0 + r;
       float x = INFINITY;  // exp2(s - inf): nothing
       int lim = 0;
@@ -140,115 +134,143 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, HILO>::kCtas)
       lim_s[r] = lim;
     }
   };
-  if (n_chunks == 1) {
-    stage_chunk(0);
-    __syncthreads();
-  }
-
   float *out = a.mass + ((int64_t)b * c.num_kv_heads + kvh) * a.mass_stride;
-  for (int it = 0; it < n_steps; it++) {
-    cp_wait<C::kStages - 2>();
-    __syncwarp();
-    issue(it + C::kStages - 1);
-    const int st = it % C::kStages;
-    const uint32_t on = live >> (kT * st) & ((1u << kT) - 1);
-    const int tok = (first + it * kWarps * kT) * kTok;
-    uint32_t kf[kT * 2][kKs][2];
-    float ksc[kT];
-    if (on) {
+  for (int ch = 0; ch < n_chunks; ch++) {
+    const int row0 = ch * C::kChunk;
+    // tokens that some row of the chunk sees
+    const int i_last = (min(row0 + C::kChunk, n_rows) - 1) / a.q.group;
+    const int tc = min(t1, len - nq + i_last + 1);
+    if (tc <= t0) continue;
+    end = (tc + kTok - 1) / kTok;
+    n_steps = (end - first + kWarps * kT - 1) / (kWarps * kT);
+    load_pages(0);
 #pragma unroll
-      for (int k = 0; k < kT; k++) {
-        const uint8_t *kt = ring + st * C::kStageBytes + k * (C::kTileBytes + 16);
-        ksc[k] = on >> k & 1 ? *reinterpret_cast<const float *>(kt + C::kTileBytes) : 0.f;
+    for (int i = 0; i < C::kStages - 1; i++) issue(i, i);
+    if (ch > 0) __syncthreads();
+    stage_chunk(row0);
+    __syncthreads();
+    const int tiles = (min(C::kChunk, n_rows - row0) + R - 1) / R;
+    for (int it = 0, st = 0; it < n_steps; it++, st = st + 1 == C::kStages ? 0 : st + 1) {
+      cp_wait<C::kStages - 2>();
+      __syncwarp();
+      issue(it + C::kStages - 1, st == 0 ? C::kStages - 1 : st - 1);
+      const uint32_t on = live >> (kT * st) & ((1u << kT) - 1);
+      const int tok = (first + it * kWarps * kT) * kTok;
+      uint4 kf[kT * 2][D / 64];
+      float ksc[kT];
+      if (on) {
 #pragma unroll
-        for (int n = 0; n < 2; n++)
+        for (int k = 0; k < kT; k++) {
+          const uint8_t *kt = ring + st * C::kStageBytes + k * (C::kTileBytes + 16);
+          ksc[k] = on >> k & 1 ? *reinterpret_cast<const float *>(kt + C::kTileBytes) : 0.f;
 #pragma unroll
-          for (int blk = 0; blk < D / 64; blk++) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(kt + k_off<D>(8 * n + g, 4 * blk + tg));
+          for (int n = 0; n < 2; n++)
 #pragma unroll
-            for (int i = 0; i < 4; i++)
-              k_frag(word(w, i), kf[2 * k + n][4 * blk + i][0], kf[2 * k + n][4 * blk + i][1]);
-          }
+            for (int blk = 0; blk < D / 64; blk++)
+              kf[2 * k + n][blk] = *reinterpret_cast<const uint4 *>(kt + k_off<D>(8 * n + g, 4 * blk + tg));
+        }
       }
-    }
-    float sum[kT * 2][2];
+      float sum[kT * 4];  // token 8 (i / 2) + 2 tg + (i & 1)
 #pragma unroll
-    for (int n = 0; n < kT * 2; n++) sum[n][0] = sum[n][1] = 0.f;
-    for (int ch = 0; ch < n_chunks; ch++) {
-      const int row0 = ch * C::kChunk;
-      if (n_chunks > 1) {
-        // rows that see none of the CTA's tokens of this step
-        const int i_last = (min(row0 + C::kChunk, n_rows) - 1) / a.q.group;
-        if (len - nq + i_last + 1 <= (t0 / kTok + it * kWarps * kT) * kTok) continue;
-        __syncthreads();
-        stage_chunk(row0);
-        __syncthreads();
-      }
+      for (int i = 0; i < kT * 4; i++) sum[i] = 0.f;
       if (!on) continue;
-      const int tiles = (min(C::kChunk, n_rows - row0) + 15) / 16;
       for (int t = 0; t < tiles; t++) {
-        // limits grow with the row; rows past the end have limit 0
-        const int last = min(row0 + 16 * t + 16, n_rows) - row0 - 1;
+        // limits grow with the row
+        const int last = min(row0 + R * t + R, n_rows) - row0 - 1;
         if (lim_s[last] <= tok) continue;
         const uint32_t *img = qimg + t * C::Q::kWords;
-        float s[kT * 2][4];
+        constexpr int kHalf = R / 8;  // rows g, and g + 8
+        float lse[kHalf], inv[kHalf];
+        int lim[kHalf];
 #pragma unroll
-        for (int n = 0; n < kT * 2; n++)
-#pragma unroll
-          for (int e = 0; e < 4; e++) s[n][e] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < kKs; ks++) {
-#pragma unroll
-          for (int v = 0; v < kL; v++) {
-            const uint4 qa = *reinterpret_cast<const uint4 *>(img + ((ks * kL + v) * 32 + lane) * 4);
-#pragma unroll
-            for (int n = 0; n < kT * 2; n++) mma16816(s[n], qa, kf[n][ks][0], kf[n][ks][1]);
-          }
+        for (int h = 0; h < kHalf; h++) {
+          lse[h] = lse_s[R * t + g + 8 * h];
+          inv[h] = inv_s[R * t + g + 8 * h];
+          lim[h] = lim_s[R * t + g + 8 * h];
         }
-        const float l0 = lse_s[16 * t + g], l1 = lse_s[16 * t + g + 8];
-        const float i0 = inv_s[16 * t + g], i1 = inv_s[16 * t + g + 8];
-        const int m0 = lim_s[16 * t + g], m1 = lim_s[16 * t + g + 8];
-        const bool cut = tok + kT * kTok > lim_s[16 * t] || last != 16 * t + 15;
+        const bool cut = tok + kT * kTok > lim_s[R * t];
+        // two 8-token blocks at a time
 #pragma unroll
-        for (int n = 0; n < kT * 2; n++) {
-          const float f0 = i0 * ksc[n >> 1], f1 = i1 * ksc[n >> 1];
+        for (int k = 0; k < kT; k++) {
+          uint32_t s[2][kL][4];
 #pragma unroll
-          for (int e = 0; e < 2; e++) {
-            float p0 = ex2(s[n][e] * f0 - l0), p1 = ex2(s[n][2 + e] * f1 - l1);
-            if (cut) {
-              const int at = tok + 8 * n + 2 * tg + e;
-              p0 = at < m0 ? p0 : 0.f;
-              p1 = at < m1 ? p1 : 0.f;
+          for (int n = 0; n < 2; n++)
+#pragma unroll
+            for (int v = 0; v < kL; v++)
+#pragma unroll
+              for (int e = 0; e < 4; e++) s[n][v][e] = kMagicBits;
+#pragma unroll
+          for (int ks = 0; ks < kKs; ks++) {
+#pragma unroll
+            for (int v = 0; v < kL; v++) {
+              const uint4 qa = *reinterpret_cast<const uint4 *>(img + ((ks * kL + v) * 32 + lane) * 4);
+#pragma unroll
+              for (int n = 0; n < 2; n++) {
+                const uint4 &w = kf[2 * k + n][ks >> 1];
+                imma(s[n][v], qa, ks & 1 ? w.z : w.x, ks & 1 ? w.w : w.y);
+              }
             }
-            sum[n][e] += p0 + p1;
           }
+#pragma unroll
+          for (int n = 0; n < 2; n++)
+#pragma unroll
+            for (int h = 0; h < kHalf; h++)
+#pragma unroll
+              for (int e = 0; e < 2; e++) {
+                const float hi = isum(s[n][0][2 * h + e]);
+                const float mid = isum(R == 8 ? s[n][0][2 + e] : s[n][1][2 * h + e]);
+                const float lo = isum(R == 8 ? s[n][1][e] : s[n][kL - 1][2 * h + e]);
+                const float x = fmaf(hi, 16384.f, fmaf(mid, 128.f, lo)) * (inv[h] * ksc[k]);
+                float p = ex2(x - lse[h]);
+                if (cut && tok + 16 * k + 8 * n + 2 * tg + e >= lim[h]) p = 0.f;
+                sum[4 * k + 2 * n + e] += p;
+              }
         }
       }
-    }
-    if (!on) continue;
+      // sums over the 8 lanes of a column, halving what each lane carries: lanes
+      // end with value (lane / 4) mod kT * 4
+      int mine = 0;
 #pragma unroll
-    for (int n = 0; n < kT * 2; n++)
+      for (int o = 16, w = kT * 2; o >= 4; o >>= 1, w >>= 1) {
+        const bool up = lane & o;
+        if (w >= 1) {
 #pragma unroll
-      for (int e = 0; e < 2; e++) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) sum[n][e] += __shfl_xor_sync(0xffffffffu, sum[n][e], o);
-        const int at = tok + 8 * n + 2 * tg + e;
-        // one lane of the eight that hold the sum writes it
-        if (g == n && at < t1 && (on >> (n >> 1) & 1)) out[at] += sum[n][e];
+          for (int i = 0; i < w; i++) {
+            const float give = up ? sum[i] : sum[i + w], keep = up ? sum[i + w] : sum[i];
+            sum[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          }
+          mine += up ? w : 0;
+        } else {
+          sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
+        }
       }
+      // kT == 1: lanes 4 apart hold the same value
+      const int at = tok + 8 * (mine >> 1) + 2 * tg + (mine & 1);
+      if ((kT == 2 || !(lane & 4)) && at < tc && (on >> (mine >> 2) & 1)) out[at] += sum[0];
+    }
+    cp_wait<0>();
+    __syncwarp();
   }
-  cp_wait<0>();
 }
 
-template <int D, bool HILO>
+template <int D, int R, bool BF16>
 cudaError_t launch(const MassArgs &a, cudaStream_t s) {
-  using C = Cfg<D, HILO>;
-  auto *k = b8_mass_kernel<D, HILO>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  using C = Cfg<D, R>;
+  auto *k = b8_mass_kernel<D, R, BF16>;
+  const int64_t rows = min((int64_t)C::kChunk, (int64_t)a.q.max_q * a.q.group);
+  const int smem = C::smem((int)(rows + R - 1) / R);
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             C::smem(C::kChunk / R));
   if (e != cudaSuccess) return e;
-  k<<<(unsigned)((int64_t)a.q.batch * a.c.num_kv_heads * a.ranges), kThreads, C::kSmem, s>>>(a);
+  k<<<(unsigned)((int64_t)a.q.batch * a.c.num_kv_heads * a.ranges), kThreads, smem, s>>>(a);
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t by_rows(const MassArgs &a, cudaStream_t s) {
+  if ((int64_t)a.q.max_q * a.q.group <= 8)
+    return a.q.bf16 ? launch<D, 8, true>(a, s) : launch<D, 8, false>(a, s);
+  return a.q.bf16 ? launch<D, 16, true>(a, s) : launch<D, 16, false>(a, s);
 }
 
 }  // namespace
@@ -267,9 +289,9 @@ cudaError_t launch_b8_mass(const kvq_b8_cache &c, const B8Queries &q, const floa
   a.range_tokens = (int)(((len + want - 1) / want + granule - 1) / granule * granule);
   a.ranges = (int)((len + a.range_tokens - 1) / a.range_tokens);
   switch (c.head_dim) {
-    case 64: return q.bf16 ? launch<64, false>(a, s) : launch<64, true>(a, s);
-    case 128: return q.bf16 ? launch<128, false>(a, s) : launch<128, true>(a, s);
-    default: return q.bf16 ? launch<256, false>(a, s) : launch<256, true>(a, s);
+    case 64: return by_rows<64>(a, s);
+    case 128: return by_rows<128>(a, s);
+    default: return by_rows<256>(a, s);
   }
 }
 

@@ -2,21 +2,23 @@
 // cache that the attention and mass kernels share.  Nothing here is part of
 // the C ABI.
 //
-// Codes are integers of at most 8 bits, exact in fp16, so both products run on
-// the fp16 tensor path (m16n8k16, fp32 accumulation).  Queries are scaled by a
-// power of two that brings the row's largest magnitude to [2^13, 2^14): a bf16
-// query is then exact in fp16 down to 2^-38 of that maximum, an fp32 query is
-// split into hi + lo, 22 bits.
+// S = q K^T runs on the integer tensor path (m16n8k32, s8 x s8 -> s32): the K
+// codes are B fragments as they lie in memory, nothing is converted.  A query
+// row is scaled by 127 * 2^14 / max|q|, rounded to integers n and split exactly
+// into int8 digits n = 2^14 H + 2^7 M + L (|M|, |L| <= 64), so its elements are
+// off by at most 2^-22 of the row's largest.  Accumulators start at the bits
+// of 1.5 * 2^23: each exact integer sum (below 2^22 for 256 dims) is an fp32
+// after one subtraction.
+// O^T = V^T P^T runs on the fp16 path (m16n8k16, fp32 accumulation): codes are
+// exact in fp16.
 //
-// A dot product does not depend on the order of its terms, so dims and tokens
-// are assigned to the fragments in the order in which a thread finds them in
-// 16-byte pieces of a row; no transpose or ldmatrix is needed:
-//   S = q K^T (A = q, B = K): k step 4 blk + w of lane (g, tg) holds dims
-//     64 blk + 16 tg + 4 w + {0, 1} and {2, 3} of token g;
-//   O^T = V^T P^T (A = V^T, B = P^T): rows g and g + 8 of m tile j are dims
-//     16 g + 2 j and 16 g + 2 j + 1 (of each 128; 8 g + 2 j for D = 64), so a
-//     lane takes 16 consecutive dims of its tokens 2 tg, 2 tg + 1, 2 tg + 8,
-//     2 tg + 9, and P^T is the accumulator of S as it stands.
+// A dot product does not depend on the order of its terms, so dims are assigned
+// to the fragments in the order in which a thread finds them:
+//   S (A = q, B = K): k step 2 blk + s of lane (g, tg) holds dims 64 blk +
+//     16 tg + 8 s + {0 .. 3} and {4 .. 7} of token g;
+//   O^T (A = V^T, B = P^T): a transposing ldmatrix over pairs of codes gives
+//     lane (g, tg) dims 16 c + 2 g and + 1 of tokens 2 tg and 2 tg + 1: rows g
+//     and g + 8 of m tile c.  P^T is the accumulator of S as it stands.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -50,17 +52,15 @@ __device__ __forceinline__ void cp_wait() {
 
 // Byte offset of 16-byte chunk `ch` of row r in a staged tile of D-byte rows.
 // Chunks of a 128-byte line are permuted so that the eight lanes of one
-// shared-memory phase hit different chunks: in the K product they read four
-// chunks of rows 2p and 2p + 1, in the V product two chunks of rows i, i + 2,
-// i + 4, i + 6.
+// shared-memory phase hit different ones: in the K product they read four
+// chunks of rows 2p and 2p + 1, a V matrix is one chunk of eight rows.
 template <int D>
 __device__ __forceinline__ int k_off(int r, int ch) {
   return r * D + 16 * (D == 64 ? ch : ch ^ (4 * (r & 1)));
 }
 template <int D>
 __device__ __forceinline__ int v_off(int r, int ch) {
-  const int at = r * (D / 16) + ch;  // chunk of the tile
-  return 16 * (at ^ (2 * ((r >> 1) & 3)));
+  return r * D + 16 * (ch ^ (D == 64 ? (r >> 1) & 3 : r & 7));
 }
 
 // bytes (sel & 0xf, (sel >> 8) & 0xf) of a sign-flipped word as two exact
@@ -90,47 +90,64 @@ __device__ __forceinline__ float query_scale(float amax) {
   return __uint_as_float((uint32_t)min(max(127 + 13 - (e - 127), 1), 253) << 23);
 }
 
-// The queries of a row tile in fragment order.  For each k step (D / 16) and
-// level (1: fp16, or hi; 2: lo) 32 lanes x 16 bytes (a0..a3).  With 8 rows and
-// two levels the low part takes rows 8..15 of the one fragment.
-template <int D, int R, bool HILO>
+// d = A(s8, 16 x 32, row) * B(s8, 32 x 8, col) + d
+__device__ __forceinline__ void imma(uint32_t (&d)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+// accumulators begin as the bits of 1.5 * 2^23 and end as an exact fp32
+constexpr uint32_t kMagicBits = 0x4B400000u;
+__device__ __forceinline__ float isum(uint32_t acc) { return __uint_as_float(acc) - 12582912.f; }
+
+// The queries of a row tile in fragment order: for each k step (D / 32) and
+// level 32 lanes x 16 bytes (a0 .. a3).  16 rows: levels H, M, L.  8 rows: one
+// fragment holds H in rows 0 .. 7 and M in rows 8 .. 15, the other L.
+template <int D, int R>
 struct QTile {
-  static constexpr int kLevels = HILO && R == 16 ? 2 : 1;
-  static constexpr int kWords = D / 16 * kLevels * 128;
+  static constexpr int kLevels = R == 16 ? 3 : 2;
+  static constexpr int kWords = D / 32 * kLevels * 128;
   static constexpr int kBytes = kWords * 4;
 };
 
-// elements 4 x of one row (fp32, scaled) into the fragment image: dims d0 ..
-// d0 + 3 of row r
-template <int D, int R, bool HILO>
+// digits of dims d0 .. d0 + 3 of row r into the fragment image
+template <int D, int R>
 __device__ __forceinline__ void q_store(uint32_t *img, int r, int d0, const float (&x)[4]) {
-  const int blk = d0 >> 6, tg = (d0 >> 4) & 3, w = (d0 >> 2) & 3, ks = 4 * blk + w;
-  uint32_t hi[2], lo[2];
+  uint32_t dig[3] = {0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 2; i++) dec::split_hilo(make_float2(x[2 * i], x[2 * i + 1]), hi[i], lo[i]);
-  const int g = r & 7, half = r >> 3;  // a0, a2: rows g; a1, a3: rows g + 8
-  constexpr int kL = QTile<D, R, HILO>::kLevels;
-  uint32_t *at = img + (ks * kL * 32 + 4 * g + tg) * 4;
-  at[half] = hi[0];
-  at[2 + half] = hi[1];
-  if (R == 8) {
-    at[1] = HILO ? lo[0] : 0u;
-    at[3] = HILO ? lo[1] : 0u;
-  } else if (HILO) {
-    at[128 + half] = lo[0];
-    at[128 + 2 + half] = lo[1];
+  for (int i = 0; i < 4; i++) {
+    const int n = __float2int_rn(x[i]);
+    const int h = (n + 8192) >> 14, rest = n - (h << 14), m = (rest + 64) >> 7, l = rest - (m << 7);
+    dig[0] |= (uint32_t)(h & 255) << (8 * i);
+    dig[1] |= (uint32_t)(m & 255) << (8 * i);
+    dig[2] |= (uint32_t)(l & 255) << (8 * i);
+  }
+  const int blk = d0 >> 6, tg = (d0 >> 4) & 3, s = (d0 >> 3) & 1, half = (d0 >> 2) & 1;
+  constexpr int kL = QTile<D, R>::kLevels;
+  const int g = r & 7;
+  uint32_t *at = img + ((2 * blk + s) * kL * 32 + 4 * g + tg) * 4 + 2 * half;
+  if (R == 8) {  // a0, a2: row g; a1, a3: row g + 8
+    at[0] = dig[0];
+    at[1] = dig[1];
+    at[128] = dig[2];
+    at[129] = 0;
+  } else {
+#pragma unroll
+    for (int v = 0; v < 3; v++) at[128 * v + (r >> 3)] = dig[v];
   }
 }
 
 // Fill the image for rows row0 .. row0 + R - 1 of a (sequence, kv head), where
 // row = query * group + head; rows at or past n_rows are zero.  inv[r] gets the
-// factor that turns a raw product into a score: scale / query_scale.  Each warp
-// takes rows warp, warp + kWarps, ...
-template <int D, int R, bool HILO>
+// factor that turns an integer product into a score in log2 units.  Each warp
+// takes rows warp, warp + n_warps, ...
+template <int D, int R, bool BF16>
 __device__ __forceinline__ void stage_queries(const B8Queries &Q, int q0, int kvh, int row0,
                                               int n_rows, int warp, int n_warps, int lane,
                                               uint32_t *img, float *inv) {
   constexpr int kPer = D / 128 > 0 ? D / 128 : 1;  // 4-dim groups of a lane
+#pragma unroll 2
   for (int r = warp; r < R; r += n_warps) {
     const int row = row0 + r;
     const bool live = row < n_rows;
@@ -144,12 +161,12 @@ __device__ __forceinline__ void stage_queries(const B8Queries &Q, int q0, int kv
       const int d0 = 4 * (lane + 32 * p);
       x[p][0] = x[p][1] = x[p][2] = x[p][3] = 0.f;
       if (live && d0 < D) {
-        if (HILO) {
-          const float4 u = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(Q.q) + at + d0));
-          x[p][0] = u.x, x[p][1] = u.y, x[p][2] = u.z, x[p][3] = u.w;
-        } else {
+        if (BF16) {
           const uint2 u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(Q.q) + at + d0));
           x[p][0] = bf16lo(u.x), x[p][1] = bf16hi(u.x), x[p][2] = bf16lo(u.y), x[p][3] = bf16hi(u.y);
+        } else {
+          const float4 u = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(Q.q) + at + d0));
+          x[p][0] = u.x, x[p][1] = u.y, x[p][2] = u.z, x[p][3] = u.w;
         }
       }
 #pragma unroll
@@ -157,16 +174,18 @@ __device__ __forceinline__ void stage_queries(const B8Queries &Q, int q0, int kv
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float f = query_scale(m);
+    // rows of values below 2^-100 score 0 beside any cache; a row with an
+    // infinity or NaN scores NaN
+    const bool tiny = m < 0x1p-100f;
+    const float f = tiny ? 0.f : __fdiv_rn(2080768.f, m);
 #pragma unroll
     for (int p = 0; p < kPer; p++) {
       const int d0 = 4 * (lane + 32 * p);
 #pragma unroll
       for (int e = 0; e < 4; e++) x[p][e] *= f;
-      if (d0 < D) q_store<D, R, HILO>(img, r, d0, x[p]);
+      if (d0 < D) q_store<D, R>(img, r, d0, x[p]);
     }
-    // scale / f in log2 units; f is a power of two, so the quotient is exact
-    if (lane == 0) inv[r] = __fdiv_rn(Q.scale * kLog2e, f);
+    if (lane == 0) inv[r] = tiny ? 0.f : m - m == 0.f ? __fdiv_rn(Q.scale * kLog2e, f) : m - m;
   }
 }
 
