@@ -20,7 +20,7 @@ constexpr int kThreads = 32 * kWarps;
 
 template <int D, int R>
 struct Cfg {
-  static constexpr int kTiles = D == 256 ? 1 : 2;   // 16-token tiles of a warp's step
+  static constexpr int kTiles = D == 256 || R == 16 ? 1 : 2;  // 16-token tiles of a warp's step
   static constexpr int kTileBytes = kTok * D;
   static constexpr int kStageBytes = kTiles * (kTileBytes + 16);  // + k_scale
   static constexpr int kStages = 3;  // 128 KB in flight or landing per SM
@@ -246,7 +246,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       // kT == 1: lanes 4 apart hold the same value
       const int at = tok + 8 * (mine >> 1) + 2 * tg + (mine & 1);
-      if ((kT == 2 || !(lane & 4)) && at < tc && (on >> (mine >> 2) & 1)) out[at] += sum[0];
+      // the token has this one writer, so the reduction at L2 (which nobody waits
+      // for) adds in a fixed order
+      if ((kT == 2 || !(lane & 4)) && at < tc && (on >> (mine >> 2) & 1)) atomicAdd(out + at, sum[0]);
     }
     cp_wait<0>();
     __syncwarp();
@@ -280,11 +282,17 @@ cudaError_t launch_b8_mass(const kvq_b8_cache &c, const B8Queries &q, const floa
   MassArgs a = {c, q, lse, mass, mass_stride, 1, 0, device_error_word()};
   const int64_t len =
       max((int64_t)1, min((int64_t)q.max_seq_len, (int64_t)c.max_blocks_per_seq * c.block_size));
-  const int64_t granule = kWarps * kTok * (c.head_dim == 256 ? 1 : 2);
+  const bool few = (int64_t)q.max_q * q.group <= 8;
+  const int64_t granule = kWarps * kTok * (c.head_dim == 256 || !few ? 1 : 2);
   const int64_t units = (int64_t)q.batch * c.num_kv_heads;
   const int64_t most = (len + granule - 1) / granule;
   const int64_t resident = kNumSMs * 2;
-  int64_t want = max((resident + units - 1) / units, min((4 * resident + units - 1) / units, (len + 2047) / 2048));
+  // few rows: about four CTAs for each that the card holds, of at least 2048
+  // tokens where that fills it once; many: the card once, as every CTA stages
+  // the rows
+  int64_t want = resident / units;
+  if (few)
+    want = max((resident + units - 1) / units, min((4 * resident + units - 1) / units, (len + 2047) / 2048));
   want = max((int64_t)1, min(want, most));
   a.range_tokens = (int)(((len + want - 1) / want + granule - 1) / granule * granule);
   a.ranges = (int)((len + a.range_tokens - 1) / a.range_tokens);
