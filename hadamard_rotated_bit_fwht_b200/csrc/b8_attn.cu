@@ -441,11 +441,11 @@ __global__ void __launch_bounds__(kCombine) b8_combine_kernel(const __grid_const
 template <int D, int R, bool HILO>
 cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
   using C = Cfg<D, R, HILO>;
-  auto *k = b8_attn_kernel<D, R, HILO>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  const cudaError_t e = allow_smem<b8_attn_kernel<D, R, HILO>>(C::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)a.q.batch * a.c.num_kv_heads * a.p.row_tiles;
-  k<<<(unsigned)(units * a.p.splits), kThreads, C::kSmem, s>>>(a);
+  b8_attn_kernel<D, R, HILO>
+      <<<(unsigned)(units * a.p.splits), kThreads, C::kSmem, s>>>(a);
   return cudaGetLastError();
 }
 

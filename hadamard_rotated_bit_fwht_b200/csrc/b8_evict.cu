@@ -10,6 +10,7 @@
 // or a CTA per kept block of a head; rows are held in registers between the
 // block's maximum and the rounding, so kept codes are read once.  Bound: HBM.
 #include "b8_common.cuh"
+#include "b8_internal.cuh"
 
 namespace kvq {
 namespace {
@@ -315,8 +316,7 @@ cudaError_t launch_b8_evict(const kvq_b8_cache &src, const kvq_b8_cache &dst, in
                        mass, mass_stride, new_lens, kept,        mass_out, mass_out_stride, device_error_word()};
   // keys of up to 48 K tokens stay in shared memory between the passes
   const int cached = min(max_seq_len, 49152);
-  cudaError_t e = cudaFuncSetAttribute(b8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       49152 * 4);
+  cudaError_t e = allow_smem<b8_select_kernel>(49152 * 4);
   if (e != cudaSuccess) return e;
   b8_select_kernel<<<batch * src.num_kv_heads, kSelThreads, cached * 4, s>>>(a, cached);
   e = cudaGetLastError();

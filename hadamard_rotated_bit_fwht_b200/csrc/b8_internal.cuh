@@ -4,7 +4,24 @@
 
 #include "kvq_internal.cuh"
 
+#include <atomic>
+
 namespace kvq {
+
+// Let kernel f use up to `bytes` of dynamic shared memory: asked of the driver
+// once per kernel and device (each instance of the template has its own set).
+template <auto f>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // q, k: heads to rotate (k.num_heads 0: none); spec.d_inv_freq set
 cudaError_t launch_rope(const kvq_rope_spec &spec, int bf16, int head_dim, int num_tokens,

@@ -258,13 +258,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <int D, int R, bool BF16>
 cudaError_t launch(const MassArgs &a, cudaStream_t s) {
   using C = Cfg<D, R>;
-  auto *k = b8_mass_kernel<D, R, BF16>;
   const int64_t rows = min((int64_t)C::kChunk, (int64_t)a.q.max_q * a.q.group);
   const int smem = C::smem((int)(rows + R - 1) / R);
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             C::smem(C::kChunk / R));
+  const cudaError_t e = allow_smem<b8_mass_kernel<D, R, BF16>>(C::smem(C::kChunk / R));
   if (e != cudaSuccess) return e;
-  k<<<(unsigned)((int64_t)a.q.batch * a.c.num_kv_heads * a.ranges), kThreads, smem, s>>>(a);
+  const unsigned ctas = (unsigned)((int64_t)a.q.batch * a.c.num_kv_heads * a.ranges);
+  b8_mass_kernel<D, R, BF16><<<ctas, kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -642,8 +642,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
 template <int D>
 cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
   using C = PCfg<D>;
-  const cudaError_t e = cudaFuncSetAttribute(b8_prefill_kernel<D>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  const cudaError_t e = allow_smem<b8_prefill_kernel<D>>(C::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)a.q.batch * a.c.num_kv_heads * a.p.row_tiles;
   b8_prefill_kernel<D><<<(unsigned)(units * a.p.splits), C::kThreads, C::kSmem, s>>>(a);

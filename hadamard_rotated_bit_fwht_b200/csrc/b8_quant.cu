@@ -207,12 +207,11 @@ static cudaError_t append(const kvq_b8_cache &c, const kvq_heads &k, const kvq_h
                           int threads, int smem, int cols, int t_new,
                           const int32_t *start_pos, const int32_t *new_lens,
                           const kvq_rope_spec &spec, const int32_t *rope_pos, cudaStream_t s) {
-  auto *f = b8_append_kernel<BF16, KEEP>;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeep);
+    const cudaError_t e = allow_smem<b8_append_kernel<BF16, KEEP>>(kKeep);
     if (e != cudaSuccess) return e;
   }
-  f<<<grid, threads, smem, s>>>(c, k, v, t_new, cols, start_pos, new_lens, spec, rope_pos,
+  b8_append_kernel<BF16, KEEP><<<grid, threads, smem, s>>>(c, k, v, t_new, cols, start_pos, new_lens, spec, rope_pos,
                                 device_error_word());
   return cudaGetLastError();
 }

@@ -222,4 +222,6 @@ def test_bindings_check_shapes_first():
         kvq.b8_append(c, z(1, 1, 2, 64), z(1, 2, 2, 64), i)
     with pytest.raises(ValueError, match="stride"):
         kvq._heads("x", z(3, 4, 2, 64)[:, :3])
-    assert kvq._heads("x", z(3, 4, 5, 64)[:, :, 1:3]).token_stride == 5 * 64
+    x = z(3, 4, 5, 64)
+    assert kvq._heads("x", x[:, :, 1:3]) == (x.data_ptr() + 4 * 64, 5 * 64, 64, 2)
+    assert kvq._heads("x", x) == (x.data_ptr(), 5 * 64, 64, 5)
