@@ -37,20 +37,22 @@ struct PCfg {
   static constexpr int kGroups = kBN / 16;
   static constexpr int kRows = 128 * kNT;
   static constexpr int kSoft = 128 * kNT;
-  static constexpr int kThreads = kSoft + 128 + 32;
+  // softmax warpgroups, the converting one, and one whose first warp issues
+  static constexpr int kThreads = kSoft + 128 + 128;
+  // registers a thread (kNT == 2): a softmax thread holds a whole row of scores.
+  // Launched with 128 each; 256 x 184 + 128 x 96 + 128 x 48 = 512 x 128.
+  static constexpr int kRegsSoft = 184, kRegsConvert = 96, kRegsIssue = 48;
   static constexpr int kQTileBytes = 128 * D * 2;
   static constexpr int kKVBytes = kBN * D * 2;
   static constexpr int kInfo = 4;                 // slots of group constants
   static constexpr int kOffK = kNT * kQTileBytes;
   static constexpr int kOffV = kOffK + 2 * kKVBytes;
-  static constexpr int kRawBytes = kBN * D;       // codes of a K or V tile as they come
-  static constexpr int kOffRaw = kOffV + 2 * kKVBytes;
-  static constexpr int kOffInfo = kOffRaw + 2 * kRawBytes;
+  static constexpr int kOffInfo = kOffV + 2 * kKVBytes;
   static constexpr int kInfoFloats = 3 * 8 + 4;   // k factor, log2 v factor, its inverse; vref
   static constexpr int kOffBar = kOffInfo + kInfo * kInfoFloats * 4;
   // k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2],
-  // o_done[2], info_full[4], drain
-  static constexpr int kBars = 19;
+  // o_done[2], info_full[4], drain, all_done[2]
+  static constexpr int kBars = 21;
   static constexpr int kOffMisc = kOffBar + kBars * 8;  // abort flag, tensor memory base
   static constexpr int kUsed = kOffMisc + 16 + 1024;    // 1024: alignment
   // one CTA per SM (it takes all of tensor memory)
@@ -123,6 +125,37 @@ __device__ __forceinline__ void t5_wait_ld(float (&v)[32]) {
       :
       : "memory");
 }
+// further loads of the same wait
+__device__ __forceinline__ void after_wait(float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile(""
+                 : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]),
+                   "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7]));
+}
+__device__ __forceinline__ void t5_ld16(uint32_t addr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void t5_wait_ld(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+        "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
+        "+f"(v[14]), "+f"(v[15])
+      :
+      : "memory");
+}
+__device__ __forceinline__ void t5_st8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
 __device__ __forceinline__ void t5_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -161,47 +194,53 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// raise mx to the largest score of two 16-token groups; in: their constants
-__device__ __forceinline__ void group_max(const float (&s)[32], const float *in, float inv,
-                                          float &mx) {
+// raise mx to the largest score of the first `left` tokens of a 16-token group
+// (all of them unless cut); in: the group's constants
+__device__ __forceinline__ void group_max(float *x, const float *in, float inv, bool cut,
+                                          int left, float &mx) {
+  if (cut) {
+    // unseen tokens repeat the first one
 #pragma unroll
-  for (int gr = 0; gr < 2; gr++) {
-    const float *x = s + 16 * gr;
-    float g0 = fmaxf(x[0], x[1]), g1 = fmaxf(x[2], x[3]);
-#pragma unroll
-    for (int e = 4; e < 16; e += 4) {
-      g0 = max3(g0, x[e], x[e + 1]);
-      g1 = max3(g1, x[e + 2], x[e + 3]);
-    }
-    // unmapped groups have a log2 factor of -inf
-    const float y = fmaxf(g0, g1) * (inv * in[gr]);
-    mx = fmaxf(mx, in[8 + gr] == -INFINITY ? -INFINITY : y);
+    for (int e = 1; e < 16; e++) x[e] = e < left ? x[e] : x[0];
   }
+  float g0 = max3(x[0], x[1], x[2]), g1 = max3(x[3], x[4], x[5]);
+  g0 = max3(g0, x[6], x[7]);
+  g1 = max3(g1, x[8], x[9]);
+  g0 = max3(g0, x[10], x[11]);
+  g1 = max3(g1, x[12], x[13]);
+  g0 = max3(g0, x[14], x[15]);
+  // unmapped groups have a log2 factor of -inf
+  const float y = fmaxf(g0, g1) * (inv * in[0]);
+  mx = fmaxf(mx, in[8] == -INFINITY || (cut && left <= 0) ? -INFINITY : y);
 }
-// two groups of scores -> p' as fp16 at `to`; l grows by their probabilities
+// a group of scores -> p' as fp16 at `to`; l grows by its probabilities.  CUT:
+// only the first `left` tokens are seen.
 template <bool CUT>
-__device__ __forceinline__ void group_exp(const float (&s)[32], const float *in, float inv, float m,
+__device__ __forceinline__ void group_exp(const float *s, const float *in, float inv, float m,
                                           int left, float &l, uint32_t to) {
-  uint32_t w[16];
+  const float f = inv * in[0], c = in[8] - m;
+  const float2 f2 = make_float2(f, f), c2 = make_float2(c, c);
+  float2 p[8];
 #pragma unroll
-  for (int gr = 0; gr < 2; gr++) {
-    const float f = inv * in[gr], c = in[8 + gr] - m;
-    const float2 f2 = make_float2(f, f), c2 = make_float2(c, c);
-    float2 sum = make_float2(0.f, 0.f);
+  for (int e = 0; e < 8; e++) p[e] = __ffma2_rn(make_float2(s[2 * e], s[2 * e + 1]), f2, c2);
 #pragma unroll
-    for (int e = 0; e < 16; e += 2) {
-      const float2 x = __ffma2_rn(make_float2(s[16 * gr + e], s[16 * gr + e + 1]), f2, c2);
-      float2 p = make_float2(ex2(x.x), ex2(x.y));
-      if (CUT) {
-        p.x = 16 * gr + e < left ? p.x : 0.f;
-        p.y = 16 * gr + e + 1 < left ? p.y : 0.f;
-      }
-      sum = add2(sum, p);
-      w[8 * gr + e / 2] = pack_f16x2(p.x, p.y);
+  for (int e = 0; e < 8; e++) p[e] = make_float2(ex2(p[e].x), ex2(p[e].y));
+  if (CUT) {
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      p[e].x = 2 * e < left ? p[e].x : 0.f;
+      p[e].y = 2 * e + 1 < left ? p[e].y : 0.f;
     }
-    l = fmaf(sum.x + sum.y, in[16 + gr], l);
   }
-  t5_st16(to, w);
+  uint32_t w[8];
+#pragma unroll
+  for (int e = 0; e < 8; e++) w[e] = pack_f16x2(p[e].x, p[e].y);
+  t5_st8(to, w);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+    for (int e = 0; e < o; e++) p[e] = add2(p[e], p[e + o]);
+  l = fmaf(p[0].x + p[0].y, in[16], l);
 }
 
 template <int D>
@@ -240,11 +279,11 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
   const uint32_t bars = base + C::kOffBar;
   const uint32_t k_full = bars, k_empty = bars + 16, v_full = bars + 32, v_empty = bars + 48,
                  s_full = bars + 64, p_full = bars + 80, o_done = bars + 96, info_full = bars + 112,
-                 drain = bars + 144;
+                 drain = bars + 144, all_done = bars + 152;
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc);
   uint32_t *tmem_at = reinterpret_cast<uint32_t *>(smem + C::kOffMisc + 4);
   float *info = reinterpret_cast<float *>(smem + C::kOffInfo);
-  constexpr int kIssueWarp = C::kThreads / 32 - 1;
+  constexpr int kIssueWarp = C::kSoft / 32 + 4;
   if (tid == 0) {
     for (int i = 0; i < 2; i++) {
       mbar_init(k_full + 8 * i, 128);
@@ -254,6 +293,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, 128);
       mbar_init(o_done + 8 * i, 1);
+      mbar_init(all_done + 8 * i, 1);
     }
     for (int i = 0; i < C::kInfo; i++) mbar_init(info_full + 8 * i, 1);
     mbar_init(drain, 1);
@@ -317,8 +357,11 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
   __syncthreads();
   t5_after();
   const uint32_t tmem = *tmem_at;
-
-  if (soft) {
+  // (every warp takes its share, idle ones too)
+  if (warp < C::kSoft / 32) {
+    if constexpr (C::kNT == 2)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoft));
+    if (soft) {
     // ---------------------------------------------------------- softmax
     const int lim = live ? max(0, len - nq + qi + 1) : 0;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // 32 lanes a warp
@@ -338,31 +381,15 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       const bool cut = __any_sync(0xffffffffu, tok + kBN > lim);
       // row maximum
       float mx = -INFINITY;
-      if (!cut) {
-        float s0[32], s1[32];
-        t5_ld32(s_at, s0);
-#pragma unroll 1
-        for (int ch = 0; ch < kBN / 32; ch += 2) {
-          t5_wait_ld(s0);
-          t5_ld32(s_at + 32 * ch + 32, s1);
-          group_max(s0, in + 2 * ch, inv, mx);
-          t5_wait_ld(s1);
-          if (ch + 2 < kBN / 32) t5_ld32(s_at + 32 * ch + 64, s0);
-          group_max(s1, in + 2 * ch + 2, inv, mx);
-        }
-      } else {
-#pragma unroll 1
-        for (int ch = 0; ch < kBN / 32; ch++) {
-          float s[32];
-          t5_ld32(s_at + 32 * ch, s);
-          t5_wait_ld(s);
+      float s[kBN / 32][32];
 #pragma unroll
-          for (int e = 0; e < 32; e++) {
-            const float y = s[e] * (inv * in[2 * ch + e / 16]);
-            if (tok + 32 * ch + e < lim && in[8 + 2 * ch + e / 16] != -INFINITY) mx = fmaxf(mx, y);
-          }
-        }
-      }
+      for (int ch = 0; ch < kBN / 32; ch++) t5_ld32(s_at + 32 * ch, s[ch]);
+      t5_wait_ld(s[0]);
+#pragma unroll
+      for (int ch = 1; ch < kBN / 32; ch++) after_wait(s[ch]);
+#pragma unroll
+      for (int gr = 0; gr < C::kGroups; gr++)
+        group_max(s[gr / 2] + 16 * (gr & 1), in + gr, inv, cut, lim - tok - 16 * gr, mx);
       const float nref = in[24];
       const bool grow = mx > m + 8.f;
       if (__any_sync(0xffffffffu, grow) || nref != vref) {
@@ -395,24 +422,18 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       }
       // probabilities, over the scores that were read
       if (!cut) {
-        float s0[32], s1[32];
-        t5_ld32(s_at, s0);
-#pragma unroll 1
-        for (int ch = 0; ch < kBN / 32; ch += 2) {
-          t5_wait_ld(s0);
-          t5_ld32(s_at + 32 * ch + 32, s1);
-          group_exp<false>(s0, in + 2 * ch, inv, m, 0, l, s_at + 16 * ch);
-          t5_wait_ld(s1);
-          if (ch + 2 < kBN / 32) t5_ld32(s_at + 32 * ch + 64, s0);
-          group_exp<false>(s1, in + 2 * ch + 2, inv, m, 0, l, s_at + 16 * ch + 16);
-        }
+#pragma unroll
+        for (int gr = 0; gr < C::kGroups; gr++)
+          group_exp<false>(s[gr / 2] + 16 * (gr & 1), in + gr, inv, m, 0, l, s_at + 8 * gr);
       } else {
+        // the tiles at the end of a row's tokens: group_max has changed the
+        // scores, so they are read again
 #pragma unroll 1
-        for (int ch = 0; ch < kBN / 32; ch++) {
-          float s[32];
-          t5_ld32(s_at + 32 * ch, s);
-          t5_wait_ld(s);
-          group_exp<true>(s, in + 2 * ch, inv, m, lim - tok - 32 * ch, l, s_at + 16 * ch);
+        for (int gr = 0; gr < C::kGroups; gr++) {
+          float x[16];
+          t5_ld16(s_at + 16 * gr, x);
+          t5_wait_ld(x);
+          group_exp<true>(x, in + gr, inv, m, lim - tok - 16 * gr, l, s_at + 8 * gr);
         }
       }
       t5_wait_st();
@@ -420,10 +441,9 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       mbar_arrive(p_full + 8 * buf);
     }
     // ---- result
-    // (a wait tells a phase from the next one only: with one row tile the last
-    // score tile says that product n - 3 is done, so n - 2 comes first)
-    if (ok && n_tiles > 1) ok = wait(o_done + 8 * wg, (n_tiles - 2) & 1);
-    if (ok && n_tiles > 0) ok = wait(o_done + 8 * wg, (n_tiles - 1) & 1);
+    // (a barrier of its own: a wait tells a phase from the next one only, and at
+    // this point o_done may be one, two or three phases on)
+    if (ok && n_tiles > 0) ok = wait(all_done + 8 * wg, 0);
     t5_after();
     const bool direct = a.p.splits == 1;
     const float nan = __int_as_float(0x7fc00000);
@@ -473,7 +493,10 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       else if (a.lse != nullptr)
         a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
     }
-  } else if (tid >= C::kSoft && warp < kIssueWarp) {
+    }
+  } else if (warp < kIssueWarp) {
+    if constexpr (C::kNT == 2)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsConvert));
     // ---------------------------------------------------------- convert
     constexpr int kPer = kBN * D / 16 / 128;  // 16-code pieces a thread has of a tile
     const int ct = tid - C::kSoft;
@@ -490,12 +513,13 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       }
       return p;
     };
-    // a thread copies and converts the same pieces, so the raw bytes need no
-    // barrier: piece i is token 32 (i % kTr) + ct / 4, dims 64 (i / kTr) +
-    // 16 (ct % 4) .. + 15
+    // piece i of a thread is token 32 (i % kTr) + ct / 4, dims 64 (i / kTr) +
+    // 16 (ct % 4) .. + 15; a tile's pieces stay in registers from their load to
+    // their conversion one tile later (staged in shared memory they would take
+    // a third of its bandwidth, which the products need)
     constexpr int kTr = kBN / 32;
     const int r4 = ct >> 2, c4 = ct & 3;
-    auto copy = [&](const int8_t *codes, uint32_t raw, int j, int slots) {
+    auto copy = [&](const int8_t *codes, int j, int slots, uint4 (&x)[kPer]) {
       // first code of the lane's group
       const int t = t0 + j * kBN + (lane % C::kGroups) * 16;
       int64_t off = -1;
@@ -505,35 +529,29 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       for (int i = 0; i < kTr; i++) {
         const int tr = 32 * i + r4;
         const int64_t o = __shfl_sync(0xffffffffu, off, tr >> 4);
-        const int8_t *src = codes + o + (tr & 15) * D + 16 * c4;
+        const uint4 *src = reinterpret_cast<const uint4 *>(codes + o + (tr & 15) * D + 16 * c4);
 #pragma unroll
-        for (int pl = 0; pl < D / 64; pl++) {
-          const uint32_t dst = raw + (((pl * kTr + i) * 128 + ct) << 4);
-          if (o >= 0)
-            cp_async16(dst, src + 64 * pl);
-          else
-            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0) : "memory");
-        }
+        for (int pl = 0; pl < D / 64; pl++)
+          x[pl * kTr + i] = o >= 0 ? __ldg(src + 4 * pl) : make_uint4(0, 0, 0, 0);
       }
-      cp_commit();
     };
-    auto put = [&](uint8_t *dst, const uint8_t *raw) {
+    auto put = [&](uint8_t *dst, const uint4 (&x)[kPer]) {
 #pragma unroll
       for (int i = 0; i < kPer; i++) {
         const int tr = 32 * (i % kTr) + r4;
         uint4 h[2];
-        widen16(*reinterpret_cast<const uint4 *>(raw + ((i * 128 + ct) << 4)), h);
+        widen16(x[i], h);
         uint8_t *at = dst + (i / kTr) * (kBN * 128) + tr * 128;
         *reinterpret_cast<uint4 *>(at + (((2 * c4) ^ (tr & 7)) << 4)) = h[0];
         *reinterpret_cast<uint4 *>(at + (((2 * c4 + 1) ^ (tr & 7)) << 4)) = h[1];
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     };
-    const uint8_t *kraw = smem + C::kOffRaw, *vraw = kraw + C::kRawBytes;
+    uint4 kx[kPer], vx[kPer];
     float vref = 0x1p-100f;
     int slots = slots_of(0), next = slots_of(1);
-    copy(c.k_codes, smem_u32(kraw), 0, slots);
-    copy(c.v_codes, smem_u32(vraw), 0, slots);
+    copy(c.k_codes, 0, slots, kx);
+    copy(c.v_codes, 0, slots, vx);
     auto scales_of = [&](int slots, float &ks, float &vs) {
       ks = vs = 0.f;
       if (warp == C::kSoft / 32 && slots >= 0) {
@@ -569,22 +587,22 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(info_full + 8 * (j & 3));
       }
-      cp_wait<1>();
       if (j >= 2 && !wait(k_empty + 8 * st, ((j - 2) >> 1) & 1)) break;
-      put(smem + C::kOffK + st * C::kKVBytes, kraw);
+      put(smem + C::kOffK + st * C::kKVBytes, kx);
       mbar_arrive(k_full + 8 * st);
-      copy(c.k_codes, smem_u32(kraw), j + 1, next);
+      copy(c.k_codes, j + 1, next, kx);
       scales_of(next, ks, vs);
-      cp_wait<1>();
       if (j >= 2 && !wait(v_empty + 8 * st, ((j - 2) >> 1) & 1)) break;
-      put(smem + C::kOffV + st * C::kKVBytes, vraw);
+      put(smem + C::kOffV + st * C::kKVBytes, vx);
       mbar_arrive(v_full + 8 * st);
-      copy(c.v_codes, smem_u32(vraw), j + 1, next);
+      copy(c.v_codes, j + 1, next, vx);
       slots = next;
       next = after;
     }
-    cp_wait<0>();
-  } else if (warp == kIssueWarp && lane == 0) {
+  } else {
+    if constexpr (C::kNT == 2)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsIssue));
+    if (warp == kIssueWarp && lane == 0) {
     // ---------------------------------------------------------- issue
     constexpr uint32_t kIdS = instr_desc(kBN, false), kIdO = instr_desc(D, true);
     bool ok = true;
@@ -618,7 +636,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
         const uint64_t vb = smem_desc(base + C::kOffV + st * C::kKVBytes + ks * 2048, kBN * 128, 1024);
         t5_mma_ts(tmem + C::kColO + t * D, p + 8 * ks, vb, kIdO, j > 0 || ks > 0);
       }
-      t5_commit(o_done + 8 * t);
+      t5_commit((j == n_tiles - 1 ? all_done : o_done) + 8 * t);
       if (t == nt - 1) t5_commit(v_empty + 8 * st);
       if (i + 2 < n_items) issue_s(i + 2);
     }
@@ -628,6 +646,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       t5_commit(drain);
       for (int n = 0; n < (1 << 20) && !dec::mbar_try(drain, 0); n++) {
       }
+    }
     }
   }
   __syncwarp();
