@@ -19,6 +19,9 @@ LIB = os.path.join(PKG, "libkvq.so")
 # is recorded in the device error word (kvq_device_errors) instead of accessed
 LIB_DEBUG = os.path.join(PKG, "libkvq_debug.so")
 
+# the binding's marshalling module (host code, built against torch)
+BIND = os.path.join(PKG, "kvq_bind.so")
+
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -43,10 +46,37 @@ def _stale(lib: str = LIB) -> bool:
 OBJ_DIR = os.path.join(ROOT, "_build", "kvq")
 
 
+def build_bind(force: bool = False) -> str:
+    """Compile the marshalling module kvq_bind.so against the running Python and
+    torch (host code only)."""
+    import sysconfig
+
+    import torch
+    src = os.path.join(CSRC, "kvq_bind.cpp")
+    if not force and os.path.exists(BIND) and all(
+            os.path.getmtime(p) <= os.path.getmtime(BIND)
+            for p in (src, os.path.join(INCLUDE, "kvq.h"))):
+        return BIND
+    t = os.path.dirname(torch.__file__)
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(t, "include"),
+           os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    tmp = BIND + f".tmp{os.getpid()}"
+    subprocess.check_call([
+        "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+        *(f"-I{p}" for p in inc), src, "-o", tmp, "-L" + os.path.join(t, "lib"),
+        "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"])
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Compile every .cu to an object in parallel (relocatable device code is
     not needed: no kernel calls across files), then link libkvq.so (or, with
-    debug=True, libkvq_debug.so with the bounds checks compiled in)."""
+    debug=True, libkvq_debug.so with the bounds checks compiled in); and the
+    marshalling module of the binding."""
+    build_bind(force and not debug)
     lib = LIB_DEBUG if debug else LIB
     if not force and not _stale(lib):
         return lib

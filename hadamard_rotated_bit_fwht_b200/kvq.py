@@ -10,8 +10,8 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import importlib.util
 import os
-import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -96,14 +96,6 @@ class B8QueriesDesc(C.Structure):
     ]
 
 
-# The same layouts for struct.pack, which builds a descriptor several times as
-# fast as assigning a Structure's fields (the calls of a decode step are short)
-_HEADS = struct.Struct("Pqqixxxx")
-_ROPE = struct.Struct("Piifxxxx")
-_QUERIES = struct.Struct("PqqixxxxiiiiPPif")
-assert (_HEADS.size, _ROPE.size, _QUERIES.size) == (
-    C.sizeof(HeadsDesc), C.sizeof(RopeDesc), C.sizeof(B8QueriesDesc))
-
 _lib = None
 
 
@@ -155,7 +147,6 @@ def lib():
         L.kvq_rope_frequencies.argtypes = [C.c_int32, C.c_double, C.c_int, C.c_double, C.c_double,
                                            C.c_double, C.c_double, C.c_void_p,
                                            C.POINTER(C.c_float)]
-        # descriptors go by address: byref of a structure, or its packed bytes
         P, i32 = C.c_void_p, C.c_int32
         L.kvq_rope.argtypes = [P, C.c_int, i32, i32, P, i32, P, P, P, P, P]
         L.kvq_b8_append.argtypes = [P, P, P, C.c_int, i32, i32, P, P, P, P, P]
@@ -168,6 +159,29 @@ def lib():
                                    C.c_int64, P]
         _lib = L
     return _lib
+
+
+_bind = None
+_BOUND = ("kvq_rope", "kvq_b8_append", "kvq_b8_gather", "kvq_b8_attn_workspace", "kvq_b8_attn",
+          "kvq_b8_attn_mass", "kvq_b8_evict")
+
+
+def bind():
+    """The marshalling module (csrc/kvq_bind.cpp), connected to the library:
+    checks of arguments, outputs and descriptors of the calls of a serving
+    step, which in Python would cost more than the kernels."""
+    global _bind
+    if _bind is None:
+        path = os.path.join(_PKG, "kvq_bind.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it with "
+                              "`python -m hadamard_rotated_bit_fwht_b200.build`")
+        spec = importlib.util.spec_from_file_location("kvq_bind", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.connect(_check, *(C.cast(getattr(lib(), f), C.c_void_p).value for f in _BOUND))
+        _bind = m
+    return _bind
 
 
 def status_string(status: int) -> str:
@@ -183,11 +197,6 @@ def _check(fn, status):
 # building a Stream object (this sits on the per-token decode path); the
 # public route where this torch build lacks the internal accessor
 _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-# the current device's index, without torch's initialisation check where the
-# build has the accessor
-_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream=None):
@@ -532,55 +541,6 @@ def octave_decode_attn(fmt: OctaveFormat, query: torch.Tensor, cache: torch.Tens
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
-def _here(**tensors):
-    """Refuse tensors that are not on the current CUDA device (the library
-    launches there); None entries are skipped."""
-    dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} must be on the current CUDA device (cuda:{dev}), "
-                             f"got {t.device}")
-
-
-def _int32(name, t, numel):
-    if t.dtype != torch.int32 or t.numel() != numel or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of {numel} values, got "
-                         f"{t.dtype} {tuple(t.shape)}")
-
-
-def _empty(like, stream, shape=None, dtype=None):
-    """An empty contiguous tensor on like's device (like's shape and dtype unless
-    given) that belongs to the stream the call runs on, so that its memory is
-    not handed out again while that stream still uses it."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return _empty(like, None, shape, dtype)
-    if shape is None:
-        return torch.empty_like(like, memory_format=torch.contiguous_format)
-    return like.new_empty(shape, dtype=dtype)
-
-
-def _heads(name, t):
-    """Address, token stride, head stride and heads of [..., heads, dim] seen as
-    tokens x heads: the leading dims must step through memory as one."""
-    n = t.shape
-    if len(n) >= 3 and t.is_contiguous():
-        return t.data_ptr(), n[-2] * n[-1], n[-1], n[-2]
-    st = t.stride()
-    if len(n) < 3 or (st[-1] != 1 and n[-1] != 1):
-        raise ValueError(f"{name} must be [..., heads, dim] with dim contiguous")
-    step, span = 0, 1
-    for d in range(len(n) - 3, -1, -1):
-        if n[d] != 1:
-            if span == 1:
-                step = st[d]
-            elif st[d] != step * span:
-                raise ValueError(f"{name}: its tokens do not lie at one stride")
-            span *= n[d]
-    # the stride of a dim of size 1 says nothing
-    return t.data_ptr(), step, st[-2] if n[-2] != 1 else 0, n[-2]
-
-
 @dataclass(frozen=True)
 class Rope:
     """A rotation of the leading 2 * len(inv_freq) dims of each head: radians
@@ -606,13 +566,6 @@ class Rope:
                                           C.byref(factor)))
         return cls(torch.from_numpy(f).to(device), interleaved, float(factor.value))
 
-    def packed(self) -> bytes:
-        """The kvq_rope_spec of this rotation."""
-        f = self.inv_freq
-        if f.dtype != torch.float64 or f.dim() != 1 or not f.is_contiguous():
-            raise ValueError("inv_freq must be a contiguous float64 vector")
-        return _ROPE.pack(f.data_ptr(), 2 * f.numel(), self.interleaved, self.factor)
-
 
 def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, rope: Rope, *,
          inverse: bool = False, q_out: torch.Tensor | None = None,
@@ -620,35 +573,8 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, rope:
     """Rotate q and k ([..., heads, dim], any token and head stride) by their
     tokens' positions (int32); returns (q_out, k_out).  q_out and k_out may be
     q and k themselves.  inverse turns the other way (kvq_rope)."""
-    if q_out is None:
-        q_out = _empty(q, stream)
-    elif q_out.shape != q.shape or q_out.dtype != q.dtype:
-        raise ValueError("q_out must have q's shape and dtype")
-    hk = hko = None
-    dev = _device()
-    here = (q.get_device() == dev and q_out.get_device() == dev
-            and positions.get_device() == dev and rope.inv_freq.get_device() == dev)
-    if k is not None:
-        if k_out is None:
-            k_out = _empty(k, stream)
-        if (k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1] or k.dtype != q.dtype
-                or k_out.shape != k.shape or k_out.dtype != k.dtype):
-            raise ValueError("k and k_out must match q's tokens, dim and dtype")
-        here = here and k.get_device() == dev and k_out.get_device() == dev
-        hk, hko = _HEADS.pack(*_heads("k", k)), _HEADS.pack(*_heads("k_out", k_out))
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    if not here:
-        _here(q=q, k=k, q_out=q_out, k_out=k_out, positions=positions, inv_freq=rope.inv_freq)
-    hq, hqo = _heads("q", q), _heads("q_out", q_out)
-    dim = q.shape[-1]
-    n = q.numel() // max(dim * hq[3], 1)
-    _int32("positions", positions, n)
-    if n:
-        _check("kvq_rope",
-               lib().kvq_rope(rope.packed(), _dtype_code(q), dim, n, positions.data_ptr(), inverse,
-                              _HEADS.pack(*hq), _HEADS.pack(*hqo), hk, hko, _stream(stream)))
-    return q_out, k_out
+    return bind().rope(q, k, positions, rope.inv_freq, rope.interleaved, rope.factor, inverse,
+                       q_out, k_out, stream)
 
 
 # --------------------------------------------------------------------------
@@ -707,7 +633,7 @@ class B8Cache:
         self._desc = B8CacheDesc(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                                  v_scales.data_ptr(), shape[1], shape[3], shape[2], shape[0],
                                  bt.data_ptr(), bt.shape[0], bt.shape[1])
-        self._ref = C.byref(self._desc)
+        self._bound = (C.addressof(self._desc), k_codes)  # what the marshalling module reads
 
     @property
     def capacity(self):
@@ -724,38 +650,11 @@ def b8_append(cache: B8Cache, k: torch.Tensor, v: torch.Tensor, start_pos: torch
     the cache at start_pos[b] + i, the first new_lens[b] tokens of each
     sequence; rope rotates k first, by the storage positions or by `positions`
     [batch, t_new] (kvq_b8_append)."""
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
-        raise ValueError("k and v must have the same [batch, t_new, Hkv, dim] shape and dtype")
-    batch, t_new, hkv, dim = k.shape
-    if hkv != cache.num_kv_heads or dim != cache.head_dim:
-        raise ValueError("k and v do not match the cache's heads")
-    dev = _device()
-    if not (cache.k_codes.get_device() == dev and k.get_device() == dev and v.get_device() == dev
-            and start_pos.get_device() == dev):
-        _here(cache=cache.k_codes, k=k, v=v, start_pos=start_pos)
-    _int32("start_pos", start_pos, batch)
-    spec = at = new = None
-    if new_lens is not None:
-        if new_lens.get_device() != dev:
-            _here(new_lens=new_lens)
-        _int32("new_lens", new_lens, batch)
-        new = new_lens.data_ptr()
+    inv_freq = inter = factor = None
     if rope is not None:
-        if rope.inv_freq.get_device() != dev:
-            _here(inv_freq=rope.inv_freq)
-        spec = rope.packed()
-    if positions is not None:
-        if rope is None:
-            raise ValueError("positions without rope")
-        _here(positions=positions)
-        _int32("positions", positions, batch * t_new)
-        at = positions.data_ptr()
-    if batch == 0 or t_new == 0:
-        return
-    _check("kvq_b8_append",
-           lib().kvq_b8_append(cache._ref, _HEADS.pack(*_heads("k", k)),
-                               _HEADS.pack(*_heads("v", v)), _dtype_code(k), batch, t_new,
-                               start_pos.data_ptr(), new, spec, at, _stream(stream)))
+        inv_freq, inter, factor = rope.inv_freq, rope.interleaved, rope.factor
+    bind().append(cache._bound, k, v, start_pos, new_lens, inv_freq, inter, factor, positions,
+                  stream)
 
 
 def b8_gather(cache: B8Cache, first: torch.Tensor, ends: torch.Tensor, count: int,
@@ -763,60 +662,17 @@ def b8_gather(cache: B8Cache, first: torch.Tensor, ends: torch.Tensor, count: in
               v_out: torch.Tensor | None = None, stream=None):
     """Stored values of tokens first[b] .. first[b] + count - 1 as (k, v), each
     [batch, count, Hkv, dim]; zeros from ends[b] on (kvq_b8_gather)."""
-    batch = first.numel()
-    shape = (batch, count, cache.num_kv_heads, cache.head_dim)
-    if k_out is None:
-        k_out = _empty(cache.k_codes, stream, shape, dtype)
-    if v_out is None:
-        v_out = _empty(k_out, stream)
-    dev = _device()
-    if not (cache.k_codes.get_device() == dev and first.get_device() == dev
-            and ends.get_device() == dev and k_out.get_device() == dev
-            and v_out.get_device() == dev):
-        _here(cache=cache.k_codes, first=first, ends=ends, k_out=k_out, v_out=v_out)
-    _int32("first", first, batch)
-    _int32("ends", ends, batch)
-    for n, t in (("k_out", k_out), ("v_out", v_out)):
-        if t.shape != shape or t.dtype != k_out.dtype or not t.is_contiguous():
-            raise ValueError(f"{n} must be a contiguous {shape} tensor")
-    _check("kvq_b8_gather",
-           lib().kvq_b8_gather(cache._ref, batch, first.data_ptr(), ends.data_ptr(), count,
-                               _dtype_code(k_out), k_out.data_ptr(), v_out.data_ptr(),
-                               _stream(stream)))
-    return k_out, v_out
-
-
-def _b8_queries(cache, q, seq_lens, max_seq_len, scale, cu_q, max_q) -> bytes:
-    """The kvq_b8_queries of a call."""
-    n, hq, dim = q.shape if q.dim() == 3 else (0, 0, -1)
-    if dim != cache.head_dim or hq % cache.num_kv_heads:
-        raise ValueError("q must be [queries, Hq, dim] with the cache's dim and Hq a multiple of "
-                         "its kv heads")
-    batch = seq_lens.numel()
-    _int32("seq_lens", seq_lens, batch)
-    cu = 0
-    if cu_q is None:
-        if n != batch:
-            raise ValueError("without cu_q there is one query per sequence")
-        max_q = 1
-    else:
-        if max_q is None:
-            raise ValueError("cu_q needs max_q")
-        _int32("cu_q", cu_q, batch + 1)
-        cu = cu_q.data_ptr()
-    dev = _device()
-    if not (cache.k_codes.get_device() == dev and q.get_device() == dev
-            and seq_lens.get_device() == dev and (cu_q is None or cu_q.get_device() == dev)):
-        _here(cache=cache.k_codes, q=q, seq_lens=seq_lens, cu_q=cu_q)
-    return _QUERIES.pack(*_heads("q", q), _dtype_code(q), batch, n, max_q, cu,
-                         seq_lens.data_ptr(), max_seq_len, scale)
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"expected float32 or bfloat16, got {dtype}")
+    return bind().gather(cache._bound, first, ends, count, dtype is torch.float32, k_out, v_out,
+                         stream)
 
 
 def b8_attn_workspace(cache: B8Cache, batch: int, num_q_heads: int, max_seq_len: int,
                       max_q: int = 1, dtype: torch.dtype = torch.bfloat16) -> int:
     """Bytes of workspace that b8_attn needs for queries of this dtype."""
     code = KVQ_BF16 if dtype == torch.bfloat16 else KVQ_F32
-    return lib().kvq_b8_attn_workspace(cache._ref, code, num_q_heads, batch, max_q, max_seq_len)
+    return lib().kvq_b8_attn_workspace(C.byref(cache.desc()), code, num_q_heads, batch, max_q, max_seq_len)
 
 
 def b8_attn(cache: B8Cache, q: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
@@ -827,31 +683,8 @@ def b8_attn(cache: B8Cache, q: torch.Tensor, seq_lens: torch.Tensor, max_seq_len
     cache: out [queries, Hq, dim] in q's dtype, and lse [queries, Hq] fp32 if
     asked for.  One query per sequence, or sequence b's are rows cu_q[b] ..
     cu_q[b + 1] - 1, at most max_q, under the causal rule (kvq_b8_attn)."""
-    d = _b8_queries(cache, q, seq_lens, max_seq_len, scale, cu_q, max_q)
-    if out is None:
-        out = _empty(q, stream)
-    else:
-        _here(out=out)
-        if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
-            raise ValueError("out must be a contiguous tensor of q's shape and dtype")
-    if lse is not None:
-        _here(lse=lse)
-        if lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous():
-            raise ValueError("lse must be a contiguous fp32 [queries, Hq] tensor")
-    elif return_lse:
-        lse = _empty(q, stream, q.shape[:2], torch.float32)
-    if workspace is None:
-        nbytes = b8_attn_workspace(cache, seq_lens.numel(), q.shape[1], max_seq_len,
-                                   1 if cu_q is None else max_q, q.dtype)
-        if nbytes:
-            workspace = _empty(q, stream, nbytes, torch.uint8)
-    else:
-        _here(workspace=workspace)
-        nbytes = workspace.numel() * workspace.element_size()
-    _check("kvq_b8_attn",
-           lib().kvq_b8_attn(cache._ref, d, out.data_ptr(), _ptr(lse), _ptr(workspace), nbytes,
-                             _stream(stream)))
-    return (out, lse) if return_lse else out
+    return bind().attn(cache._bound, q, seq_lens, max_seq_len, scale, cu_q, max_q, return_lse, out,
+                       lse, workspace, stream)
 
 
 def b8_attn_mass(cache: B8Cache, q: torch.Tensor, lse: torch.Tensor, seq_lens: torch.Tensor,
@@ -861,24 +694,7 @@ def b8_attn_mass(cache: B8Cache, q: torch.Tensor, lse: torch.Tensor, seq_lens: t
     """Add to mass [batch, Hkv, >= max_seq_len] (fp32) the attention weight that
     the queries of a b8_attn call, whose lse this is, give to each cached token
     (kvq_b8_attn_mass)."""
-    if lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous fp32 [queries, Hq] tensor")
-    _b8_mass("mass", mass, cache, seq_lens.numel(), max_seq_len)
-    d = _b8_queries(cache, q, seq_lens, max_seq_len, scale, cu_q, max_q)
-    dev = _device()
-    if lse.get_device() != dev or mass.get_device() != dev:
-        _here(lse=lse, mass=mass)
-    _check("kvq_b8_attn_mass",
-           lib().kvq_b8_attn_mass(cache._ref, d, lse.data_ptr(), mass.data_ptr(), mass.shape[2],
-                                  _stream(stream)))
-
-
-def _b8_mass(name, t, cache, batch, tokens):
-    n = t.shape
-    if (len(n) != 3 or n[0] != batch or n[1] != cache.num_kv_heads or n[2] < tokens
-            or t.dtype != torch.float32 or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous fp32 [{batch}, {cache.num_kv_heads}, "
-                         f">= {tokens}] tensor")
+    bind().mass(cache._bound, q, lse, seq_lens, max_seq_len, scale, mass, cu_q, max_q, stream)
 
 
 def b8_evict(cache: B8Cache, into: B8Cache, mass: torch.Tensor, seq_lens: torch.Tensor,
@@ -889,26 +705,8 @@ def b8_evict(cache: B8Cache, into: B8Cache, mass: torch.Tensor, seq_lens: torch.
     `into`, whose blocks must not be blocks of `cache`'s sequences.  Returns
     (lengths [batch], kept old indices [batch, Hkv, keep], their mass [batch,
     Hkv, keep] or mass_out) (kvq_b8_evict)."""
-    batch, hkv = seq_lens.numel(), cache.num_kv_heads
-    _int32("seq_lens", seq_lens, batch)
-    _b8_mass("mass", mass, cache, batch, max_seq_len)
-    dev = _device()
-    if not (cache.k_codes.get_device() == dev and into.k_codes.get_device() == dev
-            and mass.get_device() == dev and seq_lens.get_device() == dev):
-        _here(cache=cache.k_codes, into=into.k_codes, mass=mass, seq_lens=seq_lens)
-    lens = _empty(seq_lens, stream)
-    kept = _empty(seq_lens, stream, (batch, hkv, max(keep, 0)), torch.int32)
-    if mass_out is None:
-        mass_out = _empty(mass, stream, (batch, hkv, max(keep, 0)), torch.float32)
-    else:
-        _here(mass_out=mass_out)
-        _b8_mass("mass_out", mass_out, cache, batch, keep)
-    _check("kvq_b8_evict",
-           lib().kvq_b8_evict(cache._ref, into._ref, batch, seq_lens.data_ptr(), max_seq_len,
-                              mass.data_ptr(), mass.shape[2], keep, recent, sinks,
-                              lens.data_ptr(), kept.data_ptr(), mass_out.data_ptr(),
-                              mass_out.shape[2], _stream(stream)))
-    return lens, kept, mass_out
+    return bind().evict(cache._bound, into._bound, mass, seq_lens, max_seq_len, keep, recent, sinks,
+                        mass_out, stream)
 
 
 # --------------------------------------------------------------------------

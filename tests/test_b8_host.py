@@ -220,8 +220,18 @@ def test_bindings_check_shapes_first():
         kvq.b8_evict(c, c, z(1, 2, 15), i, 16, 4)
     with pytest.raises(ValueError, match="same"):
         kvq.b8_append(c, z(1, 1, 2, 64), z(1, 2, 2, 64), i)
-    with pytest.raises(ValueError, match="stride"):
-        kvq._heads("x", z(3, 4, 2, 64)[:, :3])
-    x = z(3, 4, 5, 64)
-    assert kvq._heads("x", x[:, :, 1:3]) == (x.data_ptr() + 4 * 64, 5 * 64, 64, 2)
-    assert kvq._heads("x", x) == (x.data_ptr(), 5 * 64, 64, 5)
+    with pytest.raises(ValueError, match="stride"):  # tokens at two strides
+        kvq.rope(z(3, 4, 2, 64)[:, :3], None, z(9, t=torch.int32), kvq.Rope(
+            z(16, t=torch.float64)))
+    with pytest.raises(ValueError, match="inv_freq"):
+        kvq.rope(z(3, 2, 64), None, z(3, t=torch.int32), kvq.Rope(z(16)))
+    with pytest.raises(TypeError):
+        kvq.b8_gather(c, i, i, 4, torch.float16)
+    with pytest.raises(TypeError):
+        kvq.b8_attn(c, z(1, 4, 64, t=torch.float16), i, 16, 0.1)
+    with pytest.raises(TypeError):
+        kvq.b8_attn(c, None, i, 16, 0.1)
+    with pytest.raises(TypeError):
+        kvq.b8_attn(c, z(1, 4, 64), i, 16.5, 0.1)
+    with pytest.raises(ValueError, match="32 bits"):
+        kvq.b8_attn(c, z(1, 4, 64), i, 1 << 31, 0.1)
