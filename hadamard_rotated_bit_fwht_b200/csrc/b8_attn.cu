@@ -47,9 +47,31 @@ struct Cfg {
   // the merge reuses the ring: per warp R x (D + 4) of O, then m, l and vref
   static constexpr int kRow = D + 4;
   static constexpr int kOffM = kWarps * R * kRow * 4;
-  static_assert(kOffM + kWarps * (2 * R + 1) * 4 <= kRing, "merge fits the ring");
+  // in a cluster: this CTA's merged record, read by the others
+  static constexpr int kOffRec = (kOffM + kWarps * (2 * R + 1) * 4 + 15) / 16 * 16;
+  static_assert(kOffRec + R * kRow * 4 <= kRing, "merge fits the ring");
   static_assert(kSmem * kCtas <= 227 * 1024, "shared memory per SM");
 };
+
+// ---- clusters
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// this shared-memory address in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 
 template <int D, bool HILO>
 __device__ __forceinline__ void store_out(void *out, int64_t at, float4 v) {
@@ -94,9 +116,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
   const int i_last = (min(row0 + R, n_rows) - 1) / a.q.group;
   const int hi_lim = max(0, len - nq + i_last + 1);
   const int lo_lim = max(0, len - nq + row0 / a.q.group + 1);
-  const int t0 = split * a.p.split_tokens;
-  const int t1 = min(hi_lim, t0 + a.p.split_tokens);
-  if (t0 >= t1 && split > 0) return;  // the combine kernel knows
+  // a cluster's CTAs share the tokens that there are, in whole rounds of tiles
+  const int share = a.p.cluster ? (hi_lim + a.p.splits * kWarps * kTok - 1) / (a.p.splits * kWarps * kTok) *
+                                      kWarps * kTok
+                                : a.p.split_tokens;
+  const int t0 = (int)min((int64_t)split * share, (int64_t)hi_lim);
+  const int t1 = (int)min((int64_t)hi_lim, (int64_t)t0 + share);
+  if (t0 >= t1 && split > 0 && !a.p.cluster) return;  // the combine kernel knows
 
   uint32_t *qimg = reinterpret_cast<uint32_t *>(smem + C::kOffQ);
   float *inv_s = reinterpret_cast<float *>(smem + C::kOffInv);
@@ -348,7 +374,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
     const float norm = direct ? (L > 0.f ? __fdiv_rn(1.f, L) : L == 0.f ? 0.f : L) : 1.f;
     const int i = row / a.q.group, head = kvh * a.q.group + row - i * a.q.group;
     const int64_t orow = (int64_t)(q0 + i) * a.q.num_heads + head;
-    float *rec = a.ws + ((int64_t)blockIdx.x * R + r) * (D + 4);
+    float *rec = a.p.cluster ? reinterpret_cast<float *>(smem + C::kOffRec) + r * C::kRow
+                             : a.ws + ((int64_t)blockIdx.x * R + r) * (D + 4);
     for (int d = 4 * lane; d < D; d += 128) {
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -370,6 +397,54 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
         a.lse[orow] = L == 0.f ? -INFINITY : kLn2 * (M + log2f(L));
     }
   }
+  if (!a.p.cluster) return;
+  // rows split, split + splits, ... are this CTA's to join; lane s has the
+  // state of CTA s
+  cluster_sync();
+  const uint32_t recs = smem_u32(smem + C::kOffRec);
+  for (int r = split + warp * a.p.splits; r < R; r += kWarps * a.p.splits) {
+    const int row = row0 + r;
+    if (row >= n_rows) break;
+    const uint32_t at = recs + r * C::kRow * 4;
+    float4 st = make_float4(kEmpty, 0.f, 0.f, 0.f);
+    if (lane < a.p.splits) st = ld_cluster4(in_cta(at, lane));
+    float M = st.x;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float f = ex2(st.x - M);
+    float L = lane < a.p.splits ? f * st.y : 0.f;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    M = __shfl_sync(0xffffffffu, M, 0);
+    L = __shfl_sync(0xffffffffu, L, 0);
+    const float norm = L > 0.f ? __fdiv_rn(1.f, L) : L == 0.f ? 0.f : L;
+    const int i = row / a.q.group;
+    const int64_t orow = (int64_t)(q0 + i) * a.q.num_heads + kvh * a.q.group + row - i * a.q.group;
+    float4 acc[D / 128 > 0 ? D / 128 : 1];
+#pragma unroll
+    for (int h = 0; h < (D + 127) / 128; h++) acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int c8 = 0; c8 < 8; c8++) {
+      const float fs = __shfl_sync(0xffffffffu, f, c8);
+      if (c8 < a.p.splits) {
+#pragma unroll
+        for (int h = 0; h < (D + 127) / 128; h++) {
+          if (4 * lane + 128 * h >= D) continue;
+          const float4 x = ld_cluster4(in_cta(at + 16 + 16 * lane + 512 * h, c8));
+          acc[h].x += fs * x.x, acc[h].y += fs * x.y, acc[h].z += fs * x.z, acc[h].w += fs * x.w;
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < (D + 127) / 128; h++) {
+      const int d = 4 * lane + 128 * h;
+      if (d >= D) continue;
+      acc[h].x *= norm, acc[h].y *= norm, acc[h].z *= norm, acc[h].w *= norm;
+      store_out<D, HILO>(a.out, orow * D + d, acc[h]);
+    }
+    if (lane == 0 && a.lse != nullptr) a.lse[orow] = L == 0.f ? -INFINITY : kLn2 * (M + log2f(L));
+  }
+  cluster_sync();  // the others may still read this CTA's record
 }
 
 // One CTA per row: merge its splits' records.
@@ -444,9 +519,23 @@ cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
   const cudaError_t e = allow_smem<b8_attn_kernel<D, R, HILO>>(C::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)a.q.batch * a.c.num_kv_heads * a.p.row_tiles;
-  b8_attn_kernel<D, R, HILO>
-      <<<(unsigned)(units * a.p.splits), kThreads, C::kSmem, s>>>(a);
-  return cudaGetLastError();
+  if (!a.p.cluster) {
+    b8_attn_kernel<D, R, HILO>
+        <<<(unsigned)(units * a.p.splits), kThreads, C::kSmem, s>>>(a);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * a.p.splits));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = a.p.splits;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, b8_attn_kernel<D, R, HILO>, a);
 }
 
 template <int D, bool HILO, int kCombine>
@@ -473,7 +562,7 @@ cudaError_t by_rows(const AttnArgs &a, cudaStream_t s) {
     e = a.q.bf16 ? launch<D, 8, false>(a, s) : launch<D, 8, true>(a, s);
   else
     e = a.q.bf16 ? launch<D, 16, false>(a, s) : launch<D, 16, true>(a, s);
-  if (e != cudaSuccess || a.p.splits == 1) return e;
+  if (e != cudaSuccess || a.p.splits == 1 || a.p.cluster) return e;
   // few rows of many splits want more threads a row
   if (a.p.splits > 8) return a.q.bf16 ? combine<D, false, 512>(a, s) : combine<D, true, 512>(a, s);
   return a.q.bf16 ? combine<D, false, 128>(a, s) : combine<D, true, 128>(a, s);
@@ -489,6 +578,7 @@ B8Plan plan_b8_attn(const kvq_b8_cache &c, int bf16, int group, int batch, int m
   const int64_t rows = (int64_t)max_q * group;
   const int64_t cap = (int64_t)c.max_blocks_per_seq * c.block_size;
   const int64_t len = max((int64_t)1, min((int64_t)max_seq_len, cap));
+  p.cluster = 0;
   p.prefill = bf16 && rows >= kPrefillRows;
   p.rows = p.prefill ? b8_prefill_rows(c.head_dim) : rows <= 8 ? 8 : 16;
   p.row_tiles = (int)((rows + p.rows - 1) / p.rows);
@@ -502,7 +592,16 @@ B8Plan plan_b8_attn(const kvq_b8_cache &c, int bf16, int group, int batch, int m
     const int resident = kNumSMs * (c.head_dim == 256 || p.rows == 16 ? 1 : 2);
     const int64_t full = (resident + units - 1) / units;  // splits that fill the card once
     granule = kWarps * kTok;
-    if (batch == 1) {
+    const int64_t most = (len + granule - 1) / granule;
+    // clusters where all of them fit the card at once and a CTA's share is short:
+    // they save the second kernel, but the CTAs of one all wait for its slowest
+    // (118 us by two kernels against 130 by clusters of 8 for 32 sequences of
+    // 2048 to 16384 tokens and 8 kv heads; 11.1 against 9.8 for one of 777)
+    const int64_t in_cluster = min(min((int64_t)8, most), resident / units);
+    p.cluster = in_cluster > 1 && len <= in_cluster * 2048;
+    if (p.cluster) {
+      want = in_cluster;
+    } else if (batch == 1) {
       // one length: whole waves of equal splits, as few as fill the card
       want = max((int64_t)1, resident / units);
     } else {
@@ -516,11 +615,12 @@ B8Plan plan_b8_attn(const kvq_b8_cache &c, int bf16, int group, int batch, int m
   tokens = (tokens + granule - 1) / granule * granule;
   p.split_tokens = (int)tokens;
   p.splits = (int)((len + tokens - 1) / tokens);
+  p.cluster = p.cluster && p.splits > 1;
   return p;
 }
 
 size_t b8_attn_workspace_bytes(const kvq_b8_cache &c, int batch, const B8Plan &p) {
-  if (p.splits == 1) return 0;
+  if (p.splits == 1 || p.cluster) return 0;
   return (size_t)batch * c.num_kv_heads * p.row_tiles * p.splits * p.rows * (c.head_dim + 4) * 4;
 }
 

@@ -53,6 +53,7 @@ struct B8Queries {
 struct B8Plan {
   int rows, row_tiles, splits, split_tokens;
   int prefill;  // 1: the many-row kernel
+  int cluster;  // 1: the splits of a unit are one cluster
 };
 B8Plan plan_b8_attn(const kvq_b8_cache &c, int bf16, int group, int batch, int max_q,
                     int max_seq_len);

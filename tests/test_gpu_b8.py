@@ -274,15 +274,17 @@ def test_decode(dtype, dim, group):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("block", [16, 64, 256])
-def test_decode_in_splits(dtype, block):
-    """Long enough for several ranges; lengths are clamped to max_seq_len, and a
-    sequence whose blocks are all unmapped attends to nothing."""
-    lens = [9001, 4096, 33, 500]
+@pytest.mark.parametrize("longest,clamp", [(9001, 5000), (20001, 17000)])
+def test_decode_in_splits(dtype, block, longest, clamp):
+    """Long enough for several ranges, joined in a cluster or by a second kernel;
+    lengths are clamped to max_seq_len, and a sequence whose blocks are all
+    unmapped attends to nothing."""
+    lens = [longest, 4096, 33, 500]
     c, _ = filled(41, lens, 1, 128, block, unmapped=[(3, i) for i in range((500 - 1) // block + 1)])
     q = rand(42, 4, 4, 128, dtype=dtype)
-    assert kvq.b8_attn_workspace(c, 4, 4, 9001) > 0
-    check_attention(c, q, lens, None, 9001, dtype, 0.05)
-    check_attention(c, q, [9001, 4096, -7, 500], None, 5000, dtype, 0.05)
+    assert (kvq.b8_attn_workspace(c, 4, 4, longest) > 0) == (longest > 16384)
+    check_attention(c, q, lens, None, longest, dtype, 0.05)
+    check_attention(c, q, [longest, 4096, -7, 500], None, clamp, dtype, 0.05)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -513,12 +515,16 @@ def test_streams_graphs_and_workspaces():
     """Two graphs that share a workspace replay in turn, a call on another stream
     with its own: the same results as an eager call; repeats are bit-identical."""
     c, _ = filled(131, [6000, 3000], 2, 128, 32)
+    big = kvq.B8Cache.wrap(c.k_codes, c.k_scales, c.v_codes, c.v_scales, torch.cat(
+        (c.block_table, torch.full((2, 400), -1, dtype=torch.int32, device="cuda")), 1))
+    c, M = big, 18000  # a length bound that needs a workspace
     q = rand(132, 2, 8, 128, dtype=BF16)
     lens = ints([6000, 3000])
-    want, wlse = kvq.b8_attn(c, q, lens, 6000, 0.08, return_lse=True)
-    m = torch.zeros((2, 2, 6000), device="cuda")
-    kvq.b8_attn_mass(c, q, wlse, lens, 6000, 0.08, m)
-    ws = torch.empty(kvq.b8_attn_workspace(c, 2, 8, 6000), dtype=torch.uint8, device="cuda")
+    want, wlse = kvq.b8_attn(c, q, lens, M, 0.08, return_lse=True)
+    m = torch.zeros((2, 2, M), device="cuda")
+    kvq.b8_attn_mass(c, q, wlse, lens, M, 0.08, m)
+    assert kvq.b8_attn_workspace(c, 2, 8, M) > 0
+    ws = torch.empty(kvq.b8_attn_workspace(c, 2, 8, M), dtype=torch.uint8, device="cuda")
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
     outs, graphs = [], []
@@ -527,12 +533,12 @@ def test_streams_graphs_and_workspaces():
             out, lse = torch.empty_like(q), torch.empty_like(wlse)
             mm = torch.zeros_like(m)
             qi = q.clone() if i == 0 else (q * 0.5)
-            kvq.b8_attn(c, qi, lens, 6000, 0.08, out=out, lse=lse, workspace=ws)
+            kvq.b8_attn(c, qi, lens, M, 0.08, out=out, lse=lse, workspace=ws)
             st.synchronize()
             gr = torch.cuda.CUDAGraph()
             with torch.cuda.graph(gr, stream=st):
-                kvq.b8_attn(c, qi, lens, 6000, 0.08, out=out, lse=lse, workspace=ws)
-                kvq.b8_attn_mass(c, qi, lse, lens, 6000, 0.08, mm)
+                kvq.b8_attn(c, qi, lens, M, 0.08, out=out, lse=lse, workspace=ws)
+                kvq.b8_attn_mass(c, qi, lse, lens, M, 0.08, mm)
             outs.append((out, lse, mm, qi))
             graphs.append(gr)
         for o in outs:
@@ -542,12 +548,12 @@ def test_streams_graphs_and_workspaces():
     st.synchronize()
     assert torch.equal(outs[0][0], want) and torch.equal(outs[0][1], wlse)
     assert torch.equal(outs[0][2], m + m)
-    half = kvq.b8_attn(c, outs[1][3], lens, 6000, 0.08)
+    half = kvq.b8_attn(c, outs[1][3], lens, M, 0.08)
     assert torch.equal(outs[1][0], half)
     other = torch.cuda.Stream()
     other.wait_stream(torch.cuda.current_stream())
     for _ in range(3):
-        o = kvq.b8_attn(c, q, lens, 6000, 0.08, stream=other)
+        o = kvq.b8_attn(c, q, lens, M, 0.08, stream=other)
         other.synchronize()
         assert torch.equal(o, want)
 
