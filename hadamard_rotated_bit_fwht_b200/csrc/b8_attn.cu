@@ -41,7 +41,7 @@ struct Cfg {
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   // after the ring: queries, their factors and their token limits
   static constexpr int kOffQ = kRing;
-  static constexpr int kOffInv = kOffQ + QTile<D, R>::kBytes;
+  static constexpr int kOffInv = kOffQ + QTile<D, R, !HILO>::kBytes;
   static constexpr int kOffLim = kOffInv + R * 4;
   static constexpr int kSmem = kOffLim + R * 4;
   // the merge reuses the ring: per warp R x (D + 4) of O, then m, l and vref
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
   constexpr int kNb = R / 8;       // n blocks of the second product
   constexpr int kMt = D / 16;      // m tiles of the second product
   constexpr int kKs = D / 32;      // k steps of the first product
-  constexpr int kL = QTile<D, R>::kLevels;
+  constexpr int kL = QTile<D, R, !HILO>::kLevels;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, tg = lane & 3;
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; i++) issue(i, i);
 
-  stage_queries<D, R, !HILO>(a.q, q0, kvh, row0, n_rows, warp, kWarps, lane, qimg, inv_s);
+  stage_queries<D, R, !HILO>(a.q, q0, kvh, row0, R, n_rows, warp, kWarps, lane, qimg, inv_s);
   if (tid < R) lim_s[tid] = row0 + tid < n_rows ? max(0, len - nq + (row0 + tid) / a.q.group + 1) : 0;
   __syncthreads();
   const float inv0 = inv_s[g], inv1 = R == 16 ? inv_s[R == 16 ? g + 8 : g] : 0.f;
@@ -248,10 +248,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
       for (int n = 0; n < 2; n++)
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-          const float hi = isum(s[n][0][2 * nb + e]);
-          const float mid = isum(R == 8 ? s[n][0][2 + e] : s[n][1][2 * nb + e]);
-          const float lo = isum(R == 8 ? s[n][1][e] : s[n][kL - 1][2 * nb + e]);
-          p[nb][2 * n + e] = fmaf(hi, 16384.f, fmaf(mid, 128.f, lo)) * f;
+          p[nb][2 * n + e] = score<R, !HILO>(s[n], nb, e) * f;
         }
     }
     if (tok + kTok > lo_lim || !whole) {

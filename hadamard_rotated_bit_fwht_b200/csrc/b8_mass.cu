@@ -18,19 +18,21 @@ using namespace b8;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 
-template <int D, int R>
+template <int D, int R, bool BF16>
 struct Cfg {
   static constexpr int kTiles = D == 256 || R == 16 ? 1 : 2;  // 16-token tiles of a warp's step
   static constexpr int kTileBytes = kTok * D;
   static constexpr int kStageBytes = kTiles * (kTileBytes + 16);  // + k_scale
   static constexpr int kStages = 3;  // 128 KB in flight or landing per SM
   static constexpr int kChunk = R == 8 ? 8 : 128;   // rows staged at once
-  using Q = QTile<D, R>;
+  // many bf16 rows: fp16 products, K codes converted once for all of them
+  static constexpr bool kHalf = R == 16 && BF16;
+  static constexpr int kQWords = kHalf ? HTile<D>::kWords : QTile<D, R, BF16>::kWords;
   static constexpr int kOffInv = kWarps * kStages * kStageBytes;
   static constexpr int kOffLse = kOffInv + kChunk * 4;
   static constexpr int kOffLim = kOffLse + kChunk * 4;
   static constexpr int kOffQ = kOffLim + kChunk * 4;  // last: as many row tiles as there are
-  static constexpr int smem(int row_tiles) { return kOffQ + row_tiles * Q::kBytes; }
+  static constexpr int smem(int row_tiles) { return kOffQ + row_tiles * kQWords * 4; }
   static_assert(smem(kChunk / R) <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -48,8 +50,8 @@ struct MassArgs {
 template <int D, int R, bool BF16>
 __global__ void __launch_bounds__(kThreads, 2)
     b8_mass_kernel(const __grid_constant__ MassArgs a) {
-  using C = Cfg<D, R>;
-  constexpr int kKs = D / 32, kL = C::Q::kLevels, kT = C::kTiles;
+  using C = Cfg<D, R, BF16>;
+  constexpr int kKs = D / 32, kL = QTile<D, R, BF16>::kLevels, kT = C::kTiles;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, tg = lane & 3;
@@ -116,9 +118,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int n_chunks = (n_rows + C::kChunk - 1) / C::kChunk;
   auto stage_chunk = [&](int row0) {
     const int tiles = (min(C::kChunk, n_rows - row0) + R - 1) / R;
-    for (int t = 0; t < tiles; t++)
-      stage_queries<D, R, BF16>(a.q, q0, kvh, row0 + R * t, n_rows, warp, kWarps, lane,
-                                qimg + t * C::Q::kWords, inv_s + R * t);
+    stage_queries<D, R, BF16, C::kHalf>(a.q, q0, kvh, row0, R * tiles, n_rows, warp, kWarps, lane, qimg, inv_s);
     for (int r = tid; r < R * tiles; r += kThreads) {
       const int row = row0 + r;
       float x = INFINITY;  // exp2(s - inf): nothing
@@ -156,7 +156,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       issue(it + C::kStages - 1, st == 0 ? C::kStages - 1 : st - 1);
       const uint32_t on = live >> (kT * st) & ((1u << kT) - 1);
       const int tok = (first + it * kWarps * kT) * kTok;
-      uint4 kf[kT * 2][D / 64];
+      uint4 kf[C::kHalf ? 1 : kT * 2][C::kHalf ? 1 : D / 64];       // codes
+      uint32_t kh[C::kHalf ? kT * 2 : 1][C::kHalf ? D / 16 : 1][2];  // or halves
       float ksc[kT];
       if (on) {
 #pragma unroll
@@ -166,8 +167,16 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int n = 0; n < 2; n++)
 #pragma unroll
-            for (int blk = 0; blk < D / 64; blk++)
-              kf[2 * k + n][blk] = *reinterpret_cast<const uint4 *>(kt + k_off<D>(8 * n + g, 4 * blk + tg));
+            for (int blk = 0; blk < D / 64; blk++) {
+              const uint4 w = *reinterpret_cast<const uint4 *>(kt + k_off<D>(8 * n + g, 4 * blk + tg));
+              if constexpr (C::kHalf) {
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                  k_frag(word(w, i), kh[2 * k + n][4 * blk + i][0], kh[2 * k + n][4 * blk + i][1]);
+              } else {
+                kf[2 * k + n][blk] = w;
+              }
+            }
         }
       }
       float sum[kT * 4];  // token 8 (i / 2) + 2 tg + (i & 1)
@@ -178,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         // limits grow with the row
         const int last = min(row0 + R * t + R, n_rows) - row0 - 1;
         if (lim_s[last] <= tok) continue;
-        const uint32_t *img = qimg + t * C::Q::kWords;
+        const uint32_t *img = qimg + t * C::kQWords;
         constexpr int kHalf = R / 8;  // rows g, and g + 8
         float lse[kHalf], inv[kHalf];
         int lim[kHalf];
@@ -193,21 +202,36 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int k = 0; k < kT; k++) {
           uint32_t s[2][kL][4];
+          float sh[2][4];
+          if constexpr (C::kHalf) {
 #pragma unroll
-          for (int n = 0; n < 2; n++)
+            for (int n = 0; n < 2; n++)
 #pragma unroll
-            for (int v = 0; v < kL; v++)
+              for (int e = 0; e < 4; e++) sh[n][e] = 0.f;
 #pragma unroll
-              for (int e = 0; e < 4; e++) s[n][v][e] = kMagicBits;
+            for (int ks = 0; ks < D / 16; ks++) {
+              const uint4 qa = *reinterpret_cast<const uint4 *>(img + (ks * 32 + lane) * 4);
 #pragma unroll
-          for (int ks = 0; ks < kKs; ks++) {
+              for (int n = 0; n < 2; n++)
+                mma16816(sh[n], qa, kh[2 * k + n][ks][0], kh[2 * k + n][ks][1]);
+            }
+          } else {
 #pragma unroll
-            for (int v = 0; v < kL; v++) {
-              const uint4 qa = *reinterpret_cast<const uint4 *>(img + ((ks * kL + v) * 32 + lane) * 4);
+            for (int n = 0; n < 2; n++)
 #pragma unroll
-              for (int n = 0; n < 2; n++) {
-                const uint4 &w = kf[2 * k + n][ks >> 1];
-                imma(s[n][v], qa, ks & 1 ? w.z : w.x, ks & 1 ? w.w : w.y);
+              for (int v = 0; v < kL; v++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) s[n][v][e] = kMagicBits;
+#pragma unroll
+            for (int ks = 0; ks < kKs; ks++) {
+#pragma unroll
+              for (int v = 0; v < kL; v++) {
+                const uint4 qa = *reinterpret_cast<const uint4 *>(img + ((ks * kL + v) * 32 + lane) * 4);
+#pragma unroll
+                for (int n = 0; n < 2; n++) {
+                  const uint4 &w = kf[2 * k + n][ks >> 1];
+                  imma(s[n][v], qa, ks & 1 ? w.z : w.x, ks & 1 ? w.w : w.y);
+                }
               }
             }
           }
@@ -217,10 +241,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int h = 0; h < kHalf; h++)
 #pragma unroll
               for (int e = 0; e < 2; e++) {
-                const float hi = isum(s[n][0][2 * h + e]);
-                const float mid = isum(R == 8 ? s[n][0][2 + e] : s[n][1][2 * h + e]);
-                const float lo = isum(R == 8 ? s[n][1][e] : s[n][kL - 1][2 * h + e]);
-                const float x = fmaf(hi, 16384.f, fmaf(mid, 128.f, lo)) * (inv[h] * ksc[k]);
+                float x;
+                if constexpr (C::kHalf)
+                  x = sh[n][2 * h + e];
+                else
+                  x = score<R, BF16>(s[n], h, e);
+                x *= inv[h] * ksc[k];
                 float p = ex2(x - lse[h]);
                 if (cut && tok + 16 * k + 8 * n + 2 * tg + e >= lim[h]) p = 0.f;
                 sum[4 * k + 2 * n + e] += p;
@@ -257,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 template <int D, int R, bool BF16>
 cudaError_t launch(const MassArgs &a, cudaStream_t s) {
-  using C = Cfg<D, R>;
+  using C = Cfg<D, R, BF16>;
   const int64_t rows = min((int64_t)C::kChunk, (int64_t)a.q.max_q * a.q.group);
   const int smem = C::smem((int)(rows + R - 1) / R);
   const cudaError_t e = allow_smem<b8_mass_kernel<D, R, BF16>>(C::smem(C::kChunk / R));
@@ -289,7 +315,8 @@ cudaError_t launch_b8_mass(const kvq_b8_cache &c, const B8Queries &q, const floa
   // few rows: about four CTAs for each that the card holds, of at least 2048
   // tokens where that fills it once; many: the card once, as every CTA stages
   // the rows
-  int64_t want = resident / units;
+  // (whose lengths differ: half as many again)
+  int64_t want = 3 * resident / (2 * units);
   if (few)
     want = max((resident + units - 1) / units, min((4 * resident + units - 1) / units, (len + 2047) / 2048));
   want = max((int64_t)1, min(want, most));

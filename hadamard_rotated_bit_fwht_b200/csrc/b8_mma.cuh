@@ -6,7 +6,8 @@
 // codes are B fragments as they lie in memory, nothing is converted.  A query
 // row is scaled by 127 * 2^14 / max|q|, rounded to integers n and split exactly
 // into int8 digits n = 2^14 H + 2^7 M + L (|M|, |L| <= 64), so its elements are
-// off by at most 2^-22 of the row's largest.  Accumulators start at the bits
+// off by at most 2^-22 of the row's largest; fp32 queries get a fourth digit,
+// 2^-29.  Accumulators start at the bits
 // of 1.5 * 2^23: each exact integer sum (below 2^22 for 256 dims) is an fp32
 // after one subtraction.
 // O^T = V^T P^T runs on the fp16 path (m16n8k16, fp32 accumulation): codes are
@@ -102,53 +103,87 @@ constexpr uint32_t kMagicBits = 0x4B400000u;
 __device__ __forceinline__ float isum(uint32_t acc) { return __uint_as_float(acc) - 12582912.f; }
 
 // The queries of a row tile in fragment order: for each k step (D / 32) and
-// level 32 lanes x 16 bytes (a0 .. a3).  16 rows: levels H, M, L.  8 rows: one
-// fragment holds H in rows 0 .. 7 and M in rows 8 .. 15, the other L.
-template <int D, int R>
+// level 32 lanes x 16 bytes (a0 .. a3).  16 rows: a level a digit.  8 rows: one
+// fragment holds the first digit in rows 0 .. 7 and the second in rows 8 .. 15,
+// the other the third and (BF16: zeros) the fourth.
+template <int D, int R, bool BF16>
 struct QTile {
-  static constexpr int kLevels = R == 16 ? 3 : 2;
+  static constexpr int kLevels = R == 8 ? 2 : BF16 ? 3 : 4;
   static constexpr int kWords = D / 32 * kLevels * 128;
   static constexpr int kBytes = kWords * 4;
 };
 
 // digits of dims d0 .. d0 + 3 of row r into the fragment image
-template <int D, int R>
+template <int D, int R, bool BF16>
 __device__ __forceinline__ void q_store(uint32_t *img, int r, int d0, const float (&x)[4]) {
-  uint32_t dig[3] = {0, 0, 0};
+  constexpr int kDigits = BF16 ? 3 : 4;
+  uint32_t dig[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    const int n = __float2int_rn(x[i]);
-    const int h = (n + 8192) >> 14, rest = n - (h << 14), m = (rest + 64) >> 7, l = rest - (m << 7);
-    dig[0] |= (uint32_t)(h & 255) << (8 * i);
-    dig[1] |= (uint32_t)(m & 255) << (8 * i);
-    dig[2] |= (uint32_t)(l & 255) << (8 * i);
+    int n = __float2int_rn(x[i]);
+#pragma unroll
+    for (int v = 0; v < kDigits; v++) {
+      const int s = 7 * (kDigits - 1 - v);
+      const int h = s ? (n + (1 << s >> 1)) >> s : n;
+      n -= h << s;
+      dig[v] |= (uint32_t)(h & 255) << (8 * i);
+    }
   }
   const int blk = d0 >> 6, tg = (d0 >> 4) & 3, s = (d0 >> 3) & 1, half = (d0 >> 2) & 1;
-  constexpr int kL = QTile<D, R>::kLevels;
+  constexpr int kL = QTile<D, R, BF16>::kLevels;
   const int g = r & 7;
   uint32_t *at = img + ((2 * blk + s) * kL * 32 + 4 * g + tg) * 4 + 2 * half;
   if (R == 8) {  // a0, a2: row g; a1, a3: row g + 8
     at[0] = dig[0];
     at[1] = dig[1];
     at[128] = dig[2];
-    at[129] = 0;
+    at[129] = dig[3];
   } else {
 #pragma unroll
-    for (int v = 0; v < 3; v++) at[128 * v + (r >> 3)] = dig[v];
+    for (int v = 0; v < kDigits; v++) at[128 * v + (r >> 3)] = dig[v];
   }
 }
 
-// Fill the image for rows row0 .. row0 + R - 1 of a (sequence, kv head), where
-// row = query * group + head; rows at or past n_rows are zero.  inv[r] gets the
-// factor that turns an integer product into a score in log2 units.  Each warp
-// takes rows warp, warp + n_warps, ...
-template <int D, int R, bool BF16>
+// The fp16 form for 16 rows of bf16 queries, exact down to 2^-38 of a row's
+// largest: for each k step (D / 16) 32 lanes x 16 bytes (a0 .. a3).  Step 4 blk
+// + w of lane (g, tg) holds dims 64 blk + 16 tg + 4 w + {0, 1} and {2, 3}, as
+// k_frag takes them from the codes.
+template <int D>
+struct HTile {
+  static constexpr int kWords = D / 16 * 128;
+};
+template <int D>
+__device__ __forceinline__ void q_store_half(uint32_t *img, int r, int d0, const float (&x)[4]) {
+  const int blk = d0 >> 6, tg = (d0 >> 4) & 3, w = (d0 >> 2) & 3;
+  uint32_t *at = img + ((4 * blk + w) * 32 + 4 * (r & 7) + tg) * 4 + (r >> 3);
+  at[0] = pack_f16x2(x[0], x[1]);
+  at[2] = pack_f16x2(x[2], x[3]);
+}
+
+// Raw score of row g + 8 h, column e of an accumulator set s[level][4]: the
+// digits' exact sums with their weights.
+template <int R, bool BF16>
+__device__ __forceinline__ float score(const uint32_t (*s)[4], int h, int e) {
+  const float d0 = isum(s[0][2 * h + e]);
+  const float d1 = isum(R == 8 ? s[0][2 + e] : s[1][2 * h + e]);
+  const float d2 = isum(R == 8 ? s[1][e] : s[2][2 * h + e]);
+  const float hi = fmaf(d0, 16384.f, fmaf(d1, 128.f, d2));
+  if (BF16) return hi;
+  return fmaf(hi, 128.f, isum(R == 8 ? s[1][2 + e] : s[BF16 ? 2 : 3][2 * h + e]));
+}
+
+// Fill the images (a row tile after the other) for `rows` rows from row0 on of a
+// (sequence, kv head), where row = query * group + head; rows at or past n_rows
+// are zero.  inv[r] gets the factor that turns an integer product into a score
+// in log2 units.  Each warp takes rows warp, warp + n_warps, ...
+// HALF: fp16 images for many rows over the same K fragments (q_store_half).
+template <int D, int R, bool BF16, bool HALF = false>
 __device__ __forceinline__ void stage_queries(const B8Queries &Q, int q0, int kvh, int row0,
-                                              int n_rows, int warp, int n_warps, int lane,
+                                              int rows, int n_rows, int warp, int n_warps, int lane,
                                               uint32_t *img, float *inv) {
   constexpr int kPer = D / 128 > 0 ? D / 128 : 1;  // 4-dim groups of a lane
-#pragma unroll 2
-  for (int r = warp; r < R; r += n_warps) {
+#pragma unroll 4
+  for (int r = warp; r < rows; r += n_warps) {
     const int row = row0 + r;
     const bool live = row < n_rows;
     const int i = live ? row / Q.group : 0, j = live ? row - i * Q.group : 0;
@@ -177,13 +212,17 @@ __device__ __forceinline__ void stage_queries(const B8Queries &Q, int q0, int kv
     // rows of values below 2^-100 score 0 beside any cache; a row with an
     // infinity or NaN scores NaN
     const bool tiny = m < 0x1p-100f;
-    const float f = tiny ? 0.f : __fdiv_rn(2080768.f, m);
+    const float f = HALF ? query_scale(m) : tiny ? 0.f : __fdiv_rn(BF16 ? 2080768.f : 266338304.f, m);
 #pragma unroll
     for (int p = 0; p < kPer; p++) {
       const int d0 = 4 * (lane + 32 * p);
 #pragma unroll
       for (int e = 0; e < 4; e++) x[p][e] *= f;
-      if (d0 < D) q_store<D, R>(img, r, d0, x[p]);
+      if (d0 >= D) continue;
+      if (HALF)
+        q_store_half<D>(img + r / 16 * HTile<D>::kWords, r % 16, d0, x[p]);
+      else
+        q_store<D, R, BF16>(img + r / R * QTile<D, R, BF16>::kWords, r % R, d0, x[p]);
     }
     if (lane == 0) inv[r] = tiny ? 0.f : m - m == 0.f ? __fdiv_rn(Q.scale * kLog2e, f) : m - m;
   }

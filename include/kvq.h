@@ -543,8 +543,8 @@ typedef struct {
  *   (NULL if that is 0); calls that may run at the same time need one each.
  * A query that attends to no token (or to unmapped blocks only) gives zeros
  * and an lse of -inf.  Queries enter the products with an error of at most
- * 2^-22 of the row's largest element; probabilities meet V with 22 bits for
- * KVQ_F32 queries, with 11 for KVQ_BF16. */
+ * 2^-22 (KVQ_F32: 2^-29) of the row's largest element; probabilities meet V
+ * with 11 bits (KVQ_F32: 22). */
 KVQ_API size_t kvq_b8_attn_workspace(const kvq_b8_cache *cache, kvq_dtype dtype,
                                      int32_t num_q_heads, int32_t batch, int32_t max_q,
                                      int32_t max_seq_len);
