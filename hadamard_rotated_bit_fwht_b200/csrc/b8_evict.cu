@@ -158,6 +158,15 @@ __global__ void __launch_bounds__(kSelThreads)
 // chain index -> block -> scale costs no time of its own.
 constexpr int kItems = 8;
 
+// two bytes of w as signed 16-bit values (a selector's high bit repeats the
+// byte's sign, which __byte_perm does not offer)
+template <uint32_t kSel>
+__device__ __forceinline__ uint32_t sext2(uint32_t w) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(w), "n"(kSel));
+  return r;
+}
+
 // Blocks of one run: a warp each.  Larger ones: a CTA of `runs` warps each.
 // unit: kept block + cols * (kv head + heads * sequence)
 template <int D>
@@ -251,12 +260,18 @@ __global__ void __launch_bounds__(512)
         const float sc = __shfl_sync(0xffffffffu, (p ? vs : ks)[32 * i / kPieces / 32],
                                      (lane + 32 * i) / kPieces & 31);
         const uint32_t w[4] = {raw[p][i].x, raw[p][i].y, raw[p][i].z, raw[p][i].w};
-        // the largest magnitude of the codes (rounding keeps the order)
-        uint32_t m = 0;
+        // the largest magnitude of the codes (rounding keeps the order), over
+        // their even and odd bytes as pairs of 16 bits
+        uint32_t top = 0, low = 0;
 #pragma unroll
-        for (int j = 0; j < 4; j++) m = __vmaxu4(m, __vabs4(w[j]));
-        m = __vmaxu4(m, m >> 16);
-        m = __vmaxu4(m, m >> 8) & 0xff;
+        for (int j = 0; j < 4; j++) {
+          const uint32_t even = sext2<0xA280>(w[j]), odd = sext2<0xB391>(w[j]);
+          top = __vimax3_s16x2(top, even, odd);
+          low = __vimin3_s16x2(low, even, odd);
+        }
+        const int hi = max((int)(int16_t)top, (int)top >> 16);
+        const int lo = min((int)(int16_t)low, (int)low >> 16);
+        const int m = max(hi, -lo);
         amax[p] = fmaxf(amax[p], __fmul_rn((float)m, sc));
       }
 #pragma unroll

@@ -67,9 +67,15 @@ __global__ void __launch_bounds__(kThreads, 3)
     widen8<BF16>(rb, y);
     if (p.pair >= 0) {
       const int pos = rope_pos ? __ldg(rope_pos + tok0 + row) : (int)(lo + row);
+      const Pos at = position(pos, spec.factor);
       float2 cs[8];
 #pragma unroll
-      for (int e = 0; e < 8; e++) cs[e] = turn(pos, rate[e], spec.factor);
+      for (int e = 0; e < 8; e += 2) {
+        float2 cc, ss;
+        turn2(at, rate[e], rate[e + 1], cc, ss);
+        cs[e] = make_float2(cc.x, ss.x);
+        cs[e + 1] = make_float2(cc.y, ss.y);
+      }
       rotate_piece(x, y, cs, spec.interleaved);
     }
   };

@@ -24,11 +24,12 @@ __global__ void __launch_bounds__(kThreads)
   const int nt = min(tokens_per_cta, num_tokens - t0);
   const int pairs = spec.rot_dim / 2, pieces = head_dim / 16;
   const float sign = inverse ? -1.f : 1.f;
-  for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
-    const int t = i / pairs, p = i - t * pairs;
-    float2 c = turn(__ldg(positions + t0 + t), turn_rate(__ldg(spec.d_inv_freq + p)), spec.factor);
-    c.y *= sign;
-    cs[i] = c;
+  for (int i = threadIdx.x; i < nt * pairs / 2; i += kThreads) {
+    const int t = 2 * i / pairs, p = 2 * i - t * pairs;  // pairs is a multiple of 8
+    const Pos at = position(__ldg(positions + t0 + t), spec.factor);
+    float2 c, s;
+    turn2(at, turn_rate(__ldg(spec.d_inv_freq + p)), turn_rate(__ldg(spec.d_inv_freq + p + 1)), c, s);
+    *reinterpret_cast<float4 *>(cs + 2 * i) = make_float4(c.x, s.x * sign, c.y, s.y * sign);
   }
   __syncthreads();
   const int heads = q.num_heads + k.num_heads;

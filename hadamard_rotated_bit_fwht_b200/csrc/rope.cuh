@@ -18,15 +18,48 @@ __device__ __forceinline__ uint64_t turn_rate(double w) {
   const double f = w * 0.15915494309189533577;
   return (uint64_t)__double2ll_rn((f - rint(f)) * 0x1p63) << 1;
 }
-// cos t and sin t, times factor.  The leading 32 bits of the angle become
-// half turns in [-1, 1) in fp32, whose rounding moves the angle by at most
-// 2^-25 half turns, 9.4e-8 radians: the size of fp32's own rounding of the
-// products that follow.
-__device__ __forceinline__ float2 turn(int pos, uint64_t rate, float factor) {
-  const int hi = (int)((rate * (uint64_t)(int64_t)pos) >> 32);
-  float s, c;
-  sincospif((float)hi * 0x1p-31f, &s, &c);
-  return make_float2(c * factor, s * factor);
+// A position as the multiplier of two rates and the factor's sign for sines.
+struct Pos {
+  uint32_t u;
+  float cf, sf;  // factors on cosine and sine
+};
+__device__ __forceinline__ Pos position(int pos, float factor) {
+  return {pos < 0 ? 0u - (uint32_t)pos : (uint32_t)pos, factor, pos < 0 ? -factor : factor};
+}
+// cos t and sin t of two pairs, times the factors.  The leading 32 bits of each
+// angle are cut into a quadrant and a rest of at most an eighth of a turn (30
+// bits, rounded to fp32: at most 2^-25 of pi / 4); Taylor's series on the rest
+// up to x^9 and x^8 leave 1.8e-9 and 2.5e-8 there.  CUDA's sincospif took two
+// thirds of the append kernel's instructions.
+__device__ __forceinline__ void turn2(const Pos &p, uint64_t r0, uint64_t r1, float2 &c, float2 &s) {
+  uint32_t quad[2];
+  float2 x;
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    const uint64_t r = i ? r1 : r0;
+    const uint32_t hi = __umulhi((uint32_t)r, p.u) + (uint32_t)(r >> 32) * p.u;
+    quad[i] = (hi + 0x20000000u) >> 30;
+    (i ? x.y : x.x) = (float)(int)(hi - (quad[i] << 30)) * 1.46291807926715968e-9f;  // 2 pi / 2^32
+  }
+  const float2 q = mul2(x, x);
+  auto k = [](float v) { return make_float2(v, v); };
+  float2 sn = __ffma2_rn(q, k(2.75573192e-6f), k(-1.98412698e-4f));
+  float2 cn = __ffma2_rn(q, k(2.48015873e-5f), k(-1.38888889e-3f));
+  sn = __ffma2_rn(q, sn, k(8.33333333e-3f));
+  cn = __ffma2_rn(q, cn, k(4.16666667e-2f));
+  sn = __ffma2_rn(q, sn, k(-1.66666667e-1f));
+  cn = __ffma2_rn(q, cn, k(-0.5f));
+  sn = __ffma2_rn(mul2(q, x), sn, x);
+  cn = __ffma2_rn(q, cn, k(1.f));
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    const float a = i ? cn.y : cn.x, b = i ? sn.y : sn.x;
+    const bool odd = quad[i] & 1;
+    // quadrants 0 .. 3: (c, s), (-s, c), (-c, -s), (s, -c)
+    const uint32_t cs = ((quad[i] + 1) & 2) << 30, ss = (quad[i] & 2) << 30;
+    (i ? c.y : c.x) = __uint_as_float(__float_as_uint(odd ? b : a) ^ cs) * p.cf;
+    (i ? s.y : s.x) = __uint_as_float(__float_as_uint(odd ? a : b) ^ ss) * p.sf;
+  }
 }
 
 // 8 consecutive elements in fp32, in registers; 16-byte aligned addresses
