@@ -4,9 +4,10 @@
 // Per (block, kv head) of K or V: scale = max(amax / 127, old), codes
 // rint(x / scale).  One CTA owns one block of one head, so the scale, the new
 // codes and the rescaled older codes have one writer and nothing depends on
-// an order.  The new rows are read once; between the maximum and the rounding
-// their rotated fp32 values wait in shared memory (each thread reads back what
-// it wrote).  Blocks too large for that (more than kKeep bytes) are read and
+// an order.  The new rows are read once: all of them are copied to shared
+// memory at once, and between the maximum and the rounding their rotated fp32
+// values wait there, over what they came from (a thread handles its own 16
+// elements throughout).  Blocks too large for that (more than kKeep bytes) are read and
 // rotated a second time.
 #include "b8_common.cuh"
 #include "rope.cuh"
@@ -55,12 +56,27 @@ __global__ void __launch_bounds__(kThreads, 3)
   // same dims of different rows
   const Piece p = piece(threadIdx.x & (pieces - 1), rot, spec.interleaved);
   const int row_shift = __ffs(pieces) - 1;
+  const int64_t tok0 = (int64_t)b * t_new + (lo - start);
+  extern __shared__ float4 kept[];  // [piece of the thread][4][thread]
+  if (KEEP) {
+    int n = 0;
+    for (int it = threadIdx.x; it < items; it += blockDim.x, n++) {
+      const int64_t at = (tok0 + (it >> row_shift)) * src.token_stride + h * src.head_stride;
+      const uint32_t to = dec::smem_u32(kept + (size_t)n * 4 * blockDim.x + threadIdx.x);
+      constexpr int kEach = BF16 ? 1 : 2;  // 16-byte chunks of 8 elements
+      const char *base = static_cast<const char *>(src.data);
+#pragma unroll
+      for (int k = 0; k < 2 * kEach; k++)
+        b8::cp_async16(to + k * 16 * blockDim.x,
+                       base + (at + (k < kEach ? p.a : p.b)) * (BF16 ? 2 : 4) + 16 * (k % kEach));
+    }
+    b8::cp_commit();
+  }
   uint64_t rate[8];
   if (p.pair >= 0) {
 #pragma unroll
     for (int e = 0; e < 8; e++) rate[e] = turn_rate(__ldg(spec.d_inv_freq + p.pair + e));
   }
-  const int64_t tok0 = (int64_t)b * t_new + (lo - start);
   auto turned_piece = [&](int row, const Raw8<BF16> &ra, const Raw8<BF16> &rb, float (&x)[8],
                           float (&y)[8]) {
     widen8<BF16>(ra, x);
@@ -79,16 +95,14 @@ __global__ void __launch_bounds__(kThreads, 3)
       rotate_piece(x, y, cs, spec.interleaved);
     }
   };
-  extern __shared__ float4 kept[];  // [piece of the thread][4][thread]
   auto put = [&](const float (&x)[8], const float (&y)[8], int row, float inv) {
     int8_t *at = codes + (int64_t)(r0 + row) * D;
     *reinterpret_cast<uint2 *>(at + p.a) = b8::encode8(x, inv);
     *reinterpret_cast<uint2 *>(at + p.b) = b8::encode8(y, inv);
   };
-  // every piece of the thread, kAhead at a time: f(piece number, row, x, y)
+  // every piece of the thread, kAhead at a time: f(row, x, y)
   auto each = [&](auto f) {
-    int n = 0;
-    for (int it = threadIdx.x; it < items; it += kAhead * blockDim.x, n += kAhead) {
+    for (int it = threadIdx.x; it < items; it += kAhead * blockDim.x) {
       Raw8<BF16> ra[kAhead], rb[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; k++) {
@@ -105,23 +119,39 @@ __global__ void __launch_bounds__(kThreads, 3)
         if (it + k * (int)blockDim.x < items) {
           float x[8], y[8];
           turned_piece(row, ra[k], rb[k], x, y);
-          f(n + k, row, x, y);
+          f(row, x, y);
         }
       }
     }
   };
   float amax = 0.f;
-  each([&](int n, int row, const float (&x)[8], const float (&y)[8]) {
+  auto raise = [&](const float (&x)[8], const float (&y)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; e++) amax = fmaxf(amax, fmaxf(fabsf(x[e]), fabsf(y[e])));
-    if (KEEP) {
+  };
+  if (KEEP) {
+    b8::cp_wait<0>();
+    int n = 0;
+    for (int it = threadIdx.x; it < items; it += blockDim.x, n++) {
       float4 *at = kept + (size_t)n * 4 * blockDim.x + threadIdx.x;
+      Raw8<BF16> ra, rb;
+      constexpr int kEach = BF16 ? 1 : 2;
+#pragma unroll
+      for (int k = 0; k < kEach; k++) {
+        ra.r[k] = *reinterpret_cast<const uint4 *>(at + k * blockDim.x);
+        rb.r[k] = *reinterpret_cast<const uint4 *>(at + (kEach + k) * blockDim.x);
+      }
+      float x[8], y[8];
+      turned_piece(it >> row_shift, ra, rb, x, y);
+      raise(x, y);
       at[0] = make_float4(x[0], x[1], x[2], x[3]);
       at[blockDim.x] = make_float4(x[4], x[5], x[6], x[7]);
       at[2 * blockDim.x] = make_float4(y[0], y[1], y[2], y[3]);
       at[3 * blockDim.x] = make_float4(y[4], y[5], y[6], y[7]);
     }
-  });
+  } else {
+    each([&](int, const float (&x)[8], const float (&y)[8]) { raise(x, y); });
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
@@ -141,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       put(x, y, it >> row_shift, inv);
     }
   } else {
-    each([&](int, int row, const float (&x)[8], const float (&y)[8]) { put(x, y, row, inv); });
+    each([&](int row, const float (&x)[8], const float (&y)[8]) { put(x, y, row, inv); });
   }
   // the block's earlier rows follow a scale that grew
   if (old > 0.f && scale > old) {
