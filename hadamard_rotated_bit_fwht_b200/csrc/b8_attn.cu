@@ -559,7 +559,7 @@ cudaError_t by_rows(const AttnArgs &a, cudaStream_t s) {
     e = a.q.bf16 ? launch<D, 8, false>(a, s) : launch<D, 8, true>(a, s);
   else
     e = a.q.bf16 ? launch<D, 16, false>(a, s) : launch<D, 16, true>(a, s);
-  if (e != cudaSuccess || a.p.splits == 1 || a.p.cluster) return e;
+  if (e != cudaSuccess || a.p.prefill || a.p.splits == 1 || a.p.cluster) return e;
   // few rows of many splits want more threads a row
   if (a.p.splits > 8) return a.q.bf16 ? combine<D, false, 512>(a, s) : combine<D, true, 512>(a, s);
   return a.q.bf16 ? combine<D, false, 128>(a, s) : combine<D, true, 128>(a, s);
@@ -580,32 +580,28 @@ B8Plan plan_b8_attn(const kvq_b8_cache &c, int bf16, int group, int batch, int m
   p.rows = p.prefill ? b8_prefill_rows(c.head_dim) : rows <= 8 ? 8 : 16;
   p.row_tiles = (int)((rows + p.rows - 1) / p.rows);
   const int64_t units = (int64_t)batch * c.num_kv_heads * p.row_tiles;
-  int64_t granule, want;
-  if (p.prefill) {
-    // one CTA per SM; two waves' worth where there are few units
-    granule = b8_prefill_tokens(c.head_dim);
-    want = min((int64_t)2 * kNumSMs / units, (len + 4 * granule - 1) / (4 * granule));
+  p.splits = 1, p.split_tokens = 0;
+  if (p.prefill) return p;  // cut on the device
+  const int resident = kNumSMs * (c.head_dim == 256 || p.rows == 16 ? 1 : 2);
+  const int64_t full = (resident + units - 1) / units;  // splits that fill the card once
+  const int64_t granule = kWarps * kTok;
+  const int64_t most = (len + granule - 1) / granule;
+  // clusters where all of them fit the card at once and a CTA's share is short:
+  // they save the second kernel, but the CTAs of one all wait for its slowest
+  // (118 us by two kernels against 130 by clusters of 8 for 32 sequences of
+  // 2048 to 16384 tokens and 8 kv heads; 11.1 against 9.8 for one of 777)
+  const int64_t in_cluster = min(min((int64_t)8, most), resident / units);
+  p.cluster = in_cluster > 1 && len <= in_cluster * 2048;
+  int64_t want;
+  if (p.cluster) {
+    want = in_cluster;
+  } else if (batch == 1) {
+    // one length: whole waves of equal splits, as few as fill the card
+    want = max((int64_t)1, resident / units);
   } else {
-    const int resident = kNumSMs * (c.head_dim == 256 || p.rows == 16 ? 1 : 2);
-    const int64_t full = (resident + units - 1) / units;  // splits that fill the card once
-    granule = kWarps * kTok;
-    const int64_t most = (len + granule - 1) / granule;
-    // clusters where all of them fit the card at once and a CTA's share is short:
-    // they save the second kernel, but the CTAs of one all wait for its slowest
-    // (118 us by two kernels against 130 by clusters of 8 for 32 sequences of
-    // 2048 to 16384 tokens and 8 kv heads; 11.1 against 9.8 for one of 777)
-    const int64_t in_cluster = min(min((int64_t)8, most), resident / units);
-    p.cluster = in_cluster > 1 && len <= in_cluster * 2048;
-    if (p.cluster) {
-      want = in_cluster;
-    } else if (batch == 1) {
-      // one length: whole waves of equal splits, as few as fill the card
-      want = max((int64_t)1, resident / units);
-    } else {
-      // lengths differ: about four CTAs for each that the card holds at once, of
-      // at least 16 tiles a warp where that leaves one CTA for each
-      want = min((4 * (int64_t)resident + units - 1) / units, max(full, (len + 2047) / 2048));
-    }
+    // lengths differ: about four CTAs for each that the card holds at once, of
+    // at least 16 tiles a warp where that leaves one CTA for each
+    want = min((4 * (int64_t)resident + units - 1) / units, max(full, (len + 2047) / 2048));
   }
   want = max((int64_t)1, min(want, (len + granule - 1) / granule));
   int64_t tokens = (len + want - 1) / want;
@@ -617,6 +613,7 @@ B8Plan plan_b8_attn(const kvq_b8_cache &c, int bf16, int group, int batch, int m
 }
 
 size_t b8_attn_workspace_bytes(const kvq_b8_cache &c, int batch, const B8Plan &p) {
+  if (p.prefill) return b8_prefill_workspace(c.head_dim);
   if (p.splits == 1 || p.cluster) return 0;
   return (size_t)batch * c.num_kv_heads * p.row_tiles * p.splits * p.rows * (c.head_dim + 4) * 4;
 }

@@ -16,9 +16,9 @@ struct AttnArgs {
   int polls;  // limit of the bounded waits
 };
 
-// rows of a CTA and tokens of a tile of the many-row kernel
+// rows of a CTA of the many-row kernel, and its workspace
 int b8_prefill_rows(int head_dim);
-int b8_prefill_tokens(int head_dim);
+size_t b8_prefill_workspace(int head_dim);
 cudaError_t launch_b8_prefill(const AttnArgs &a, cudaStream_t s);
 
 }  // namespace kvq

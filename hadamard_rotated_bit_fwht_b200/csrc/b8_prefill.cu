@@ -243,6 +243,129 @@ __device__ __forceinline__ void group_exp(const float *s, const float *in, float
   l = fmaf(p[0].x + p[0].y, in[16], l);
 }
 
+// ---- work
+// A CTA per unit (row tile of a sequence and kv head), the longest sequences
+// first, in whole waves of the card's SMs; the units of the last, partial wave
+// (all of them where there are fewer units than SMs) are cut along their tokens
+// into as many pieces as fill it, and a second kernel joins those.  Without the
+// cut a prompt chunk of 336 units ended on 40 SMs: 491 us.  Lengths live on the
+// device, so each CTA finds its unit: it ranks the sequences and counts their
+// row tiles.
+constexpr int kLeast = 4;  // tiles of a piece
+struct Job {
+  int b, kvh, rt;      // b < 0: nothing to do
+  int piece, pieces;   // of the unit's tokens (some may be empty)
+  int tail;            // index among the cut units, -1 if not one
+};
+// behind the records of the pieces (at most one an SM): what each cut unit is
+__device__ __forceinline__ int4 *metas(const AttnArgs &a, int rows, int dim) {
+  return reinterpret_cast<int4 *>(a.ws + (int64_t)kNumSMs * rows * (dim + 4));
+}
+template <class C>
+__device__ Job find_job(const AttnArgs &a) {
+  __shared__ int ids[C::kThreads], tiles[C::kThreads];  // sequences by rank, their row tiles
+  const int tid = threadIdx.x, batch = a.q.batch, hkv = a.c.num_kv_heads;
+  Job j = {-1, 0, 0, 0, 1, -1};
+  int4 *meta = metas(a, C::kRows, a.c.head_dim);
+  if (batch > C::kThreads) {  // as they come, uncut
+    int u = blockIdx.x;
+    if (u == 0 && tid < kNumSMs) meta[tid].x = -1;
+    j.kvh = u % hkv;
+    u /= hkv;
+    j.rt = a.p.row_tiles - 1 - u % a.p.row_tiles;
+    u /= a.p.row_tiles;
+    j.b = u < batch ? u : -1;
+    return j;
+  }
+  if (tid < batch) {
+    const int mine = seq_len(a.q, a.c, tid);
+    int rank = 0, q0;
+    for (int o = 0; o < batch; o++) {
+      const int l = seq_len(a.q, a.c, o);
+      rank += l > mine || (l == mine && o < tid);
+    }
+    ids[rank] = tid;
+    tiles[rank] = (query_range(a.q, tid, q0) * a.q.group + C::kRows - 1) / C::kRows;
+  }
+  __syncthreads();
+  int units = 0;
+  for (int s = 0; s < batch; s++) units += tiles[s] * hkv;
+  const int whole = units / kNumSMs * kNumSMs, rest = units - whole;
+  const int pieces = rest ? kNumSMs / rest : 1;
+  if (blockIdx.x == 0 && tid < kNumSMs && (tid >= rest || pieces == 1)) meta[tid].x = -1;
+  int u = blockIdx.x;
+  if (u >= whole) {
+    u -= whole;
+    if (pieces > 1) {
+      j.tail = u / pieces;
+      j.piece = u % pieces;
+      j.pieces = pieces;
+      u = j.tail;
+    }
+    u += whole;
+  }
+  for (int s = 0; s < batch; s++) {
+    const int n = tiles[s] * hkv;
+    if (u < n) {
+      j.b = ids[s];
+      j.rt = tiles[s] - 1 - u / hkv;
+      j.kvh = u % hkv;
+      break;
+    }
+    u -= n;
+  }
+  return j;
+}
+
+// One warp per row of the cut units: join the pieces' records.
+// grid: 8 rows + rows / 8 * cut unit
+template <int D>
+__global__ void __launch_bounds__(256) b8_join_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int kRows = PCfg<D>::kRows;
+  const int lane = threadIdx.x & 31;
+  const int unit = blockIdx.x / (kRows / 8);
+  const int r = blockIdx.x % (kRows / 8) * 8 + (threadIdx.x >> 5);
+  dec::grid_dependency_wait();
+  const int4 m = metas(a, kRows, D)[unit];
+  if (m.x < 0) return;
+  int q0;
+  const int n_rows = query_range(a.q, m.x, q0) * a.q.group, row = m.z * kRows + r;
+  if (row >= n_rows) return;
+  const int n = m.w & 0xffff, slots = m.w >> 16;
+  const float *rec = a.ws + ((int64_t)unit * slots * kRows + r) * (D + 4);
+  constexpr int64_t kStep = (int64_t)kRows * (D + 4);
+  float M = -1e30f, L = 0.f;
+  for (int s = 0; s < n; s++) M = fmaxf(M, rec[s * kStep]);
+  constexpr int kPer = D / 128 > 0 ? D / 128 : 1;
+  float4 acc[kPer];
+#pragma unroll
+  for (int h = 0; h < kPer; h++) acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < n; s++) {
+    const float f = ex2(rec[s * kStep] - M);
+    L += f * rec[s * kStep + 1];
+#pragma unroll
+    for (int h = 0; h < kPer; h++) {
+      if (4 * lane + 128 * h >= D) continue;
+      const float4 x = *reinterpret_cast<const float4 *>(rec + s * kStep + 4 + 4 * lane + 128 * h);
+      acc[h].x += f * x.x, acc[h].y += f * x.y, acc[h].z += f * x.z, acc[h].w += f * x.w;
+    }
+  }
+  const float norm = L > 0.f ? __fdiv_rn(1.f, L) : L == 0.f ? 0.f : L;
+  const int i = row / a.q.group;
+  const int64_t orow = (int64_t)(q0 + i) * a.q.num_heads + m.y * a.q.group + row - i * a.q.group;
+#pragma unroll
+  for (int h = 0; h < kPer; h++) {
+    const int d = 4 * lane + 128 * h;
+    if (d >= D) continue;
+    const __nv_bfloat162 u = __floats2bfloat162_rn(acc[h].x * norm, acc[h].y * norm);
+    const __nv_bfloat162 v = __floats2bfloat162_rn(acc[h].z * norm, acc[h].w * norm);
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + orow * D + d) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v));
+  }
+  if (lane == 0 && a.lse != nullptr) a.lse[orow] = L == 0.f ? -INFINITY : kLn2 * (M + log2f(L));
+}
+
 template <int D>
 __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
     b8_prefill_kernel(const __grid_constant__ AttnArgs a) {
@@ -253,14 +376,9 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const kvq_b8_cache &c = a.c;
 
-  // split fastest, then (kv head, sequence); row tiles from the last, whose
-  // token ranges are the longest, to the first
-  int u = blockIdx.x;
-  const int split = u % a.p.splits;
-  u /= a.p.splits;
-  const int bh = u % (a.q.batch * c.num_kv_heads);
-  const int rt = a.p.row_tiles - 1 - u / (a.q.batch * c.num_kv_heads);
-  const int kvh = bh % c.num_kv_heads, b = bh / c.num_kv_heads;
+  const Job job = find_job<C>(a);
+  if (job.b < 0) return;
+  const int b = job.b, kvh = job.kvh, rt = job.rt;
   int q0;
   const int nq = query_range(a.q, b, q0);
   const int n_rows = nq * a.q.group, row0 = rt * C::kRows;
@@ -268,9 +386,14 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
   const int len = seq_len(a.q, c, b);
   const int i_last = (min(row0 + C::kRows, n_rows) - 1) / a.q.group;
   const int hi_lim = max(0, len - nq + i_last + 1);
-  const int t0 = split * a.p.split_tokens;  // a multiple of kBN
-  const int t1 = min(hi_lim, t0 + a.p.split_tokens);
-  if (t0 >= t1 && split > 0) return;
+  const int all_tiles = (hi_lim + kBN - 1) / kBN;
+  const int per = max(kLeast, (all_tiles + job.pieces - 1) / job.pieces);
+  const int pieces = max(1, (all_tiles + per - 1) / per);  // that hold work
+  if (job.piece >= pieces) return;
+  if (job.tail >= 0 && job.piece == 0 && tid == 0)
+    metas(a, C::kRows, D)[job.tail] = make_int4(pieces > 1 ? b : -1, kvh, rt, job.pieces << 16 | pieces);
+  const int t0 = job.piece * per * kBN;
+  const int t1 = min(hi_lim, t0 + per * kBN);
   const int nt = C::kNT == 2 && n_rows - row0 > 128 ? 2 : 1;
   const int n_tiles = t1 > t0 ? (t1 - t0 + kBN - 1) / kBN : 0;
   const int n_items = n_tiles * nt;
@@ -445,14 +568,13 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
     // this point o_done may be one, two or three phases on)
     if (ok && n_tiles > 0) ok = wait(all_done + 8 * wg, 0);
     t5_after();
-    const bool direct = a.p.splits == 1;
+    const bool direct = pieces == 1;
     const float nan = __int_as_float(0x7fc00000);
     float norm = vref * 0x1p-6f;
     if (direct) norm = l > 0.f ? norm / l : l == 0.f ? 0.f : l;
     if (!ok) norm = m = l = nan;
     const int64_t orow = (int64_t)(q0 + qi) * a.q.num_heads + head;
-    const int64_t unit = (int64_t)bh * a.p.row_tiles + rt;
-    float *rec = a.ws + ((unit * a.p.splits + split) * C::kRows + wg * 128 + r) * (D + 4);
+    float *rec = a.ws + (((int64_t)job.tail * job.pieces + job.piece) * C::kRows + wg * 128 + r) * (D + 4);
 #pragma unroll 1
     for (int ch = 0; ch < D / 32; ch++) {
       float o[32];
@@ -661,17 +783,31 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
 template <int D>
 cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
   using C = PCfg<D>;
-  const cudaError_t e = allow_smem<b8_prefill_kernel<D>>(C::kSmem);
+  cudaError_t e = allow_smem<b8_prefill_kernel<D>>(C::kSmem);
   if (e != cudaSuccess) return e;
+  // the units that there may be, and the pieces that the last ones are cut into
   const int64_t units = (int64_t)a.q.batch * a.c.num_kv_heads * a.p.row_tiles;
-  b8_prefill_kernel<D><<<(unsigned)(units * a.p.splits), C::kThreads, C::kSmem, s>>>(a);
-  return cudaGetLastError();
+  b8_prefill_kernel<D><<<(unsigned)(units + kNumSMs), C::kThreads, C::kSmem, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kNumSMs * C::kRows / 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, b8_join_kernel<D>, a);
 }
 
 }  // namespace
 
 int b8_prefill_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }
-int b8_prefill_tokens(int head_dim) { return head_dim == 256 ? 64 : 128; }
+size_t b8_prefill_workspace(int head_dim) {
+  return (size_t)kNumSMs * (b8_prefill_rows(head_dim) * (head_dim + 4) * 4 + sizeof(int4));
+}
 
 cudaError_t launch_b8_prefill(const AttnArgs &a, cudaStream_t s) {
   switch (a.c.head_dim) {

@@ -158,15 +158,15 @@ def test_attention_refusals(L, p16):
         assert call(queries(p16, **kw)) == INVALID, kw
     assert call(queries(p16), out=None) == INVALID
     assert call(queries(p16), out=p16 + 8) == INVALID
-    big = cache_desc(p16, cols=512)
-    q = queries(p16, max_len=8192)
-    need = L.kvq_b8_attn_workspace(C.byref(big), 1, 4, 2, 1, 8192)
+    big = cache_desc(p16, cols=2048)
+    q = queries(p16, max_len=32768)
+    need = L.kvq_b8_attn_workspace(C.byref(big), 1, 4, 2, 1, 32768)
     assert need > 0
     assert call(q, d=big) == WORKSPACE
     assert call(q, d=big, ws=p16, n=need - 1) == WORKSPACE
     assert call(q, d=big, ws=p16 + 4, n=need) == WORKSPACE
-    assert L.kvq_b8_attn_workspace(C.byref(big), 1, 3, 2, 1, 8192) == 0
-    assert L.kvq_b8_attn_workspace(C.byref(cache_desc(p16, dim=80)), 1, 4, 2, 1, 8192) == 0
+    assert L.kvq_b8_attn_workspace(C.byref(big), 1, 3, 2, 1, 32768) == 0
+    assert L.kvq_b8_attn_workspace(C.byref(cache_desc(p16, dim=80)), 1, 4, 2, 1, 32768) == 0
     wide = queries(p16, batch=2, total=1 << 30, max_q=(1 << 31) - 1, cu=p16)
     assert call(wide) == UNSUPPORTED
 

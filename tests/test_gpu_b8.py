@@ -331,6 +331,19 @@ def check_mass(m, m0, r, q, lse, real, at, scale, a, dtype):
         assert torch.equal(m[b, :, n:].cpu(), m0[b, :, n:])
 
 
+@pytest.mark.parametrize("batch,hkv,group,most_q,longest", [
+    (6, 8, 4, 220, 700),    # more units than SMs: whole ones, and cut ones at the end
+    (600, 1, 16, 8, 90)])   # more sequences than a CTA ranks
+def test_prompts_of_many_units(batch, hkv, group, most_q, longest):
+    g = np.random.default_rng(batch)
+    lens = g.integers(0, longest + 1, batch).tolist()
+    nq = np.minimum(g.integers(0, most_q + 1, batch), 10 + np.array(lens)).tolist()
+    lens[0], nq[0] = longest, most_q
+    c, _ = filled(55, lens, hkv, 64, 16)
+    q = rand(56, sum(nq), hkv * group, 64, dtype=BF16)
+    check_attention(c, q, lens, [0] + np.cumsum(nq).tolist(), longest, BF16, 0.125)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("dim,group", [(64, 1), (128, 4), (128, 16), (256, 5)])
 def test_mass_of_decode_steps(dtype, dim, group):
