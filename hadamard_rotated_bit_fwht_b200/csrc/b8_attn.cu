@@ -28,7 +28,6 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kEmpty = -1e30f;  // running maximum before any token
 constexpr float kSlack = 8.f;
-constexpr int64_t kPrefillRows = 64;
 
 // HILO: fp32 output, probabilities as fp16 hi + lo
 template <int D, int R, bool HILO>
@@ -576,7 +575,13 @@ B8Plan plan_b8_attn(const kvq_b8_cache &c, int bf16, int group, int batch, int m
   const int64_t cap = (int64_t)c.max_blocks_per_seq * c.block_size;
   const int64_t len = max((int64_t)1, min((int64_t)max_seq_len, cap));
   p.cluster = 0;
-  p.prefill = bf16 && rows >= kPrefillRows;
+  // The many-row kernel costs a tile of 256 rows whatever it holds, this file's
+  // one of 16: 16 sequences of 4096 tokens, 8 kv heads, D = 128, 32 rows 114 us
+  // against 96, 48 rows 114 against 139.  Where there is less to do, its longer
+  // set-up counts: one such sequence 25 us against 18 at 64 rows, 25 against 27
+  // at 128.
+  const int64_t tiles16 = (int64_t)batch * c.num_kv_heads * ((rows + 15) / 16);
+  p.prefill = bf16 && (rows >= 128 || (rows >= 48 && tiles16 * len >= 400000));
   p.rows = p.prefill ? b8_prefill_rows(c.head_dim) : rows <= 8 ? 8 : 16;
   p.row_tiles = (int)((rows + p.rows - 1) / p.rows);
   const int64_t units = (int64_t)batch * c.num_kv_heads * p.row_tiles;

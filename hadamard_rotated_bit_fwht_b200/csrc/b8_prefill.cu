@@ -334,21 +334,41 @@ __global__ void __launch_bounds__(256) b8_join_kernel(const __grid_constant__ At
   const int n = m.w & 0xffff, slots = m.w >> 16;
   const float *rec = a.ws + ((int64_t)unit * slots * kRows + r) * (D + 4);
   constexpr int64_t kStep = (int64_t)kRows * (D + 4);
+  // lane l: states of pieces l, l + 32, ... (at most kNumSMs)
+  constexpr int kMost = (kNumSMs + 31) / 32;
+  float pm[kMost], pl[kMost];
   float M = -1e30f, L = 0.f;
-  for (int s = 0; s < n; s++) M = fmaxf(M, rec[s * kStep]);
+#pragma unroll
+  for (int i = 0; i < kMost; i++) {
+    const int s = lane + 32 * i;
+    const float2 x = s < n ? *reinterpret_cast<const float2 *>(rec + s * kStep) : make_float2(-1e30f, 0.f);
+    pm[i] = x.x, pl[i] = x.y;
+    M = fmaxf(M, x.x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+  for (int i = 0; i < kMost; i++) {
+    pm[i] = ex2(pm[i] - M);
+    L += pm[i] * pl[i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   constexpr int kPer = D / 128 > 0 ? D / 128 : 1;
   float4 acc[kPer];
 #pragma unroll
   for (int h = 0; h < kPer; h++) acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int s = 0; s < n; s++) {
-    const float f = ex2(rec[s * kStep] - M);
-    L += f * rec[s * kStep + 1];
 #pragma unroll
-    for (int h = 0; h < kPer; h++) {
-      if (4 * lane + 128 * h >= D) continue;
-      const float4 x = *reinterpret_cast<const float4 *>(rec + s * kStep + 4 + 4 * lane + 128 * h);
-      acc[h].x += f * x.x, acc[h].y += f * x.y, acc[h].z += f * x.z, acc[h].w += f * x.w;
+  for (int i = 0; i < kMost; i++) {
+#pragma unroll 8
+    for (int s = 32 * i; s < min(n, 32 * i + 32); s++) {
+      const float f = __shfl_sync(0xffffffffu, pm[i], s & 31);
+#pragma unroll
+      for (int h = 0; h < kPer; h++) {
+        if (4 * lane + 128 * h >= D) continue;
+        const float4 x = *reinterpret_cast<const float4 *>(rec + s * kStep + 4 + 4 * lane + 128 * h);
+        acc[h].x += f * x.x, acc[h].y += f * x.y, acc[h].z += f * x.z, acc[h].w += f * x.w;
+      }
     }
   }
   const float norm = L > 0.f ? __fdiv_rn(1.f, L) : L == 0.f ? 0.f : L;

@@ -29,7 +29,7 @@ __device__ __forceinline__ Pos position(int pos, float factor) {
 // cos t and sin t of two pairs, times the factors.  The leading 32 bits of each
 // angle are cut into a quadrant and a rest of at most an eighth of a turn (30
 // bits, rounded to fp32: at most 2^-25 of pi / 4); Taylor's series on the rest
-// up to x^9 and x^8 leave 1.8e-9 and 2.5e-8 there.  CUDA's sincospif took two
+// up to x^9 and x^10 leave 1.8e-9 and 1.1e-10 there.  CUDA's sincospif took two
 // thirds of the append kernel's instructions.
 __device__ __forceinline__ void turn2(const Pos &p, uint64_t r0, uint64_t r1, float2 &c, float2 &s) {
   uint32_t quad[2];
@@ -44,7 +44,8 @@ __device__ __forceinline__ void turn2(const Pos &p, uint64_t r0, uint64_t r1, fl
   const float2 q = mul2(x, x);
   auto k = [](float v) { return make_float2(v, v); };
   float2 sn = __ffma2_rn(q, k(2.75573192e-6f), k(-1.98412698e-4f));
-  float2 cn = __ffma2_rn(q, k(2.48015873e-5f), k(-1.38888889e-3f));
+  float2 cn = __ffma2_rn(q, k(-2.75573192e-7f), k(2.48015873e-5f));
+  cn = __ffma2_rn(q, cn, k(-1.38888889e-3f));
   sn = __ffma2_rn(q, sn, k(8.33333333e-3f));
   cn = __ffma2_rn(q, cn, k(4.16666667e-2f));
   sn = __ffma2_rn(q, sn, k(-1.66666667e-1f));
@@ -130,29 +131,25 @@ __device__ __forceinline__ Piece piece(int j, int rot, int interleaved) {
   p.pair = turned ? 8 * j : -1;
   return p;
 }
-// rotate a piece in place; cs[i] = (cos, sin) of pair i of the piece
+// rotate a piece in place; cs[i] = (cos, sin) of pair i of the piece.  Products
+// and sums are rounded one by one, as the plain formula does: what is quantized
+// next then falls on the same side of a code's border.
+__device__ __forceinline__ void rotate_pair(float &a, float &b, float2 cs) {
+  const float x = a, y = b;
+  a = __fsub_rn(__fmul_rn(x, cs.x), __fmul_rn(y, cs.y));
+  b = __fadd_rn(__fmul_rn(y, cs.x), __fmul_rn(x, cs.y));
+}
 __device__ __forceinline__ void rotate_piece(float (&u)[8], float (&v)[8], const float2 *cs,
                                              int interleaved) {
   if (interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      const float a = u[2 * i], b = u[2 * i + 1];
-      u[2 * i] = a * cs[i].x - b * cs[i].y;
-      u[2 * i + 1] = b * cs[i].x + a * cs[i].y;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const float a = v[2 * i], b = v[2 * i + 1];
-      v[2 * i] = a * cs[4 + i].x - b * cs[4 + i].y;
-      v[2 * i + 1] = b * cs[4 + i].x + a * cs[4 + i].y;
+      rotate_pair(u[2 * i], u[2 * i + 1], cs[i]);
+      rotate_pair(v[2 * i], v[2 * i + 1], cs[4 + i]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      const float a = u[i], b = v[i];
-      u[i] = a * cs[i].x - b * cs[i].y;
-      v[i] = b * cs[i].x + a * cs[i].y;
-    }
+    for (int i = 0; i < 8; i++) rotate_pair(u[i], v[i], cs[i]);
   }
 }
 
