@@ -23,6 +23,31 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
+// Launch that may begin while the kernel before it on the stream ends; cluster:
+// CTAs of a cluster (1: none).  Every thread of f starts with
+// dec::grid_dependency_wait(): it waits until that kernel is done and its writes
+// are visible, so stream order is kept and only the launch itself overlaps.  What such kernels read they read past
+// L1 (__ldcg, cp.async.cg) or with plain loads, not through the read-only path,
+// whose data must not change while a grid exists.
+template <class... P, class... A>
+cudaError_t launch_early(void (*f)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
+                         int cluster, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, f, P(args)...);
+}
+
 // q, k: heads to rotate (k.num_heads 0: none); spec.d_inv_freq set
 cudaError_t launch_rope(const kvq_rope_spec &spec, int bf16, int head_dim, int num_tokens,
                         const int32_t *positions, int inverse, const kvq_heads &q,

@@ -185,10 +185,10 @@ __device__ __forceinline__ void stage_queries(const B8Queries &Q, int q0, int kv
       x[p][0] = x[p][1] = x[p][2] = x[p][3] = 0.f;
       if (live && d0 < D) {
         if (BF16) {
-          const uint2 u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(Q.q) + at + d0));
+          const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(Q.q) + at + d0));
           x[p][0] = bf16lo(u.x), x[p][1] = bf16hi(u.x), x[p][2] = bf16lo(u.y), x[p][3] = bf16hi(u.y);
         } else {
-          const float4 u = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(Q.q) + at + d0));
+          const float4 u = __ldcg(reinterpret_cast<const float4 *>(static_cast<const float *>(Q.q) + at + d0));
           x[p][0] = u.x, x[p][1] = u.y, x[p][2] = u.z, x[p][3] = u.w;
         }
       }
@@ -223,15 +223,15 @@ __device__ __forceinline__ int query_range(const B8Queries &Q, int b, int &q0) {
     q0 = b;
     return b < Q.total_q ? 1 : 0;
   }
-  q0 = __ldg(Q.cu_q + b);
-  const int64_t n = (int64_t)__ldg(Q.cu_q + b + 1) - q0;
+  q0 = __ldcg(Q.cu_q + b);
+  const int64_t n = (int64_t)__ldcg(Q.cu_q + b + 1) - q0;
   if (q0 < 0 || n <= 0 || n > Q.max_q || q0 + n > Q.total_q) return 0;
   return (int)n;
 }
 
 __device__ __forceinline__ int seq_len(const B8Queries &Q, const kvq_b8_cache &c, int b) {
   const int64_t cap = (int64_t)c.max_blocks_per_seq * c.block_size;
-  return (int)min((int64_t)min(max(__ldg(Q.seq_lens + b), 0), Q.max_seq_len), cap);
+  return (int)min((int64_t)min(max(__ldcg(Q.seq_lens + b), 0), Q.max_seq_len), cap);
 }
 
 }  // namespace b8
