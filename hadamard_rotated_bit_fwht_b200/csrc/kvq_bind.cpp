@@ -349,7 +349,8 @@ PyObject *bind_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
   OnStream on(a[11], dev);
   Tensor on_, ln, wn;
   if (out == nullptr) on_ = empty(q.sizes(), q.scalar_type(), dev), out = &on_;
-  const bool want_lse = a[7] == Py_True;
+  const int want_lse = PyObject_IsTrue(a[7]);
+  if (want_lse < 0) throw python_error();
   if (lse == nullptr && want_lse)
     ln = empty({q.size(0), q.size(1)}, at::kFloat, dev), lse = &ln;
   size_t bytes = 0;

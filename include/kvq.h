@@ -498,7 +498,7 @@ typedef struct {
  * rint(x * (1 / scale)) in [-127, 127]; where the scale grew, the codes of the
  * block's earlier tokens become rint(code * (old / scale)).  All in fp32,
  * rounding to nearest even.  Rows behind the new tokens stay as they were.  A
- * block must not be reached by two sequences of one call. */
+ * block must not be reached twice in one call, by two sequences or by one. */
 KVQ_API kvq_status kvq_b8_append(const kvq_b8_cache *cache, const kvq_heads *k,
                                  const kvq_heads *v, kvq_dtype dtype, int32_t batch,
                                  int32_t t_new, const int32_t *d_start_pos,

@@ -110,7 +110,7 @@ class Cache:
 
 
 def attention(ref, q, lens, cu, scale):
-    """fp64 (out, lse, a) per query row; a: the largest scale * sum |q| |k| of
+    """fp64 (out, lse, a) per query row; a: the largest |scale| * sum |q| |k| of
     the row, which bounds the rounding of its scores."""
     hq = q.shape[1]
     out = torch.zeros(q.shape, dtype=torch.float64)
@@ -132,7 +132,7 @@ def attention(ref, q, lens, cu, scale):
             out[cu[b]:cu[b + 1], h] = p @ v[kh]
             lse[cu[b]:cu[b + 1], h] = t
             if n:
-                a[cu[b]:cu[b + 1], h] = (x.abs() @ k[kh].abs().T * scale).amax(1)
+                a[cu[b]:cu[b + 1], h] = (x.abs() @ k[kh].abs().T).amax(1) * abs(scale)
     return out, lse, a
 
 

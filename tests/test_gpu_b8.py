@@ -378,6 +378,92 @@ def test_wide_ranges_of_values(dtype):
     check_attention(c, q.to(dtype), [400, 390], None, 400, dtype, 0.1)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("scale", [0.0, -0.125])
+def test_other_scales(dtype, scale):
+    c, _ = filled(73, [300, 40], 1, 64, 32)
+    for nq in (1, 40):
+        q = rand(74, 2 * nq, 4, 64, dtype=dtype)
+        check_attention(c, q, [300, 40], [0, nq, 2 * nq], 300, dtype, scale)
+
+
+def test_nothing_cached_and_one_kv_head_for_many():
+    """No token at all, by every kernel; 144 query heads on one kv head."""
+    c, _ = filled(75, [64, 64], 1, 128, 64)
+    for dtype, nq, hq in ((BF16, 1, 4), (F32, 1, 16), (F32, 9, 4), (BF16, 70, 2)):
+        q = rand(76, 2 * nq, hq, 128, dtype=dtype)
+        for lens, most in (([0, 0], 64), ([64, 64], 0)):
+            out, lse = kvq.b8_attn(c, q, ints(lens), most, 0.1, cu_q=ints([0, nq, 2 * nq]), max_q=nq,
+                                   return_lse=True)
+            assert not out.any() and (lse == -math.inf).all()
+    for dtype in (BF16, F32):
+        check_attention(c, rand(77, 2, 144, 128, dtype=dtype), [64, 33], None, 64, dtype, 0.08)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("nq", [1, 3, 80])
+def test_a_bad_query_spoils_its_own_row_only(dtype, nq):
+    c, _ = filled(78, [500], 1, 128, 16)
+    q = rand(79, nq, 2, 128, dtype=dtype)
+    kw = dict(cu_q=ints([0, nq]), max_q=nq, return_lse=True)
+    want, wlse = kvq.b8_attn(c, q, ints([500]), 500, 0.1, **kw)
+    for v in (math.nan, math.inf):
+        bad = q.clone()
+        bad[0, 1, 7] = v
+        out, lse = kvq.b8_attn(c, bad, ints([500]), 500, 0.1, **kw)
+        assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])
+        ok = torch.ones((nq, 2), dtype=torch.bool, device="cuda")
+        ok[0, 1] = False
+        assert torch.equal(out[ok], want[ok]) and torch.equal(lse[ok], wlse[ok])
+
+
+def test_two_calls_at_once():
+    """Prompts, decodes and weights on two streams at the same time."""
+    c, _ = filled(83, [3000, 2500], 2, 128, 64)
+    q = rand(84, 600, 8, 128, dtype=BF16)
+    p = dict(cu_q=ints([0, 300, 600]), max_q=300, return_lse=True)
+    lens, d = ints([3000, 2500]), q[:2].contiguous()
+    want, wlse = kvq.b8_attn(c, q, lens, 3000, 0.08, **p)
+    dec, dlse = kvq.b8_attn(c, d, lens, 3000, 0.08, return_lse=True)
+    m0 = torch.zeros((2, 2, 3000), device="cuda")
+    kvq.b8_attn_mass(c, d, dlse, lens, 3000, 0.08, m0)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(6):
+        for st in streams:
+            a = kvq.b8_attn(c, q, lens, 3000, 0.08, stream=st, **p)[0]
+            b, l = kvq.b8_attn(c, d, lens, 3000, 0.08, stream=st, return_lse=True)
+            with torch.cuda.stream(st):
+                m = torch.zeros((2, 2, 3000), device="cuda")
+            kvq.b8_attn_mass(c, d, l, lens, 3000, 0.08, m, stream=st)
+            got.append((a, b, m))
+    torch.cuda.synchronize()
+    for a, b, m in got:
+        assert torch.equal(a, want) and torch.equal(b, dec) and torch.equal(m, m0)
+
+
+def test_wait_timeout_is_reported_and_recovers():
+    """A wait of the many-row kernel that gives up at once leaves NaN and a flag;
+    the next call with the default limit is exact again."""
+    c, _ = filled(85, [4000], 2, 128, 64)
+    q = rand(86, 512, 8, 128, dtype=BF16)
+    run = lambda: kvq.b8_attn(c, q, ints([4000]), 4000, 0.08, cu_q=ints([0, 512]), max_q=512)
+    want = run()
+    assert kvq.device_errors() == 0
+    kvq.set_wait_limit(0)
+    try:
+        got = run()
+        flags = kvq.device_errors()
+    finally:
+        kvq.set_wait_limit(-1)
+    assert flags & kvq.KVQ_DEVERR_WAIT_TIMEOUT
+    assert torch.isnan(got).any()
+    again = run()
+    assert kvq.device_errors() == 0
+    assert torch.equal(again, want)
+
+
 def test_bad_query_ranges_have_no_queries():
     c, _ = filled(81, [50, 50, 50], 1, 64, 16)
     q = rand(82, 12, 2, 64)
