@@ -662,9 +662,11 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
     constexpr int kTr = kBN / 32;
     const int r4 = ct >> 2, c4 = ct & 3;
     auto copy = [&](const int8_t *codes, int j, int slots, uint4 (&x)[kPer]) {
-      // first code of the lane's group
+      // first code of the lane's group; groups without a block take block 0's
+      // codes, which meet probabilities of 0 (a choice between a load and a zero
+      // would wait for the load right here)
       const int t = t0 + j * kBN + (lane % C::kGroups) * 16;
-      int64_t off = -1;
+      int64_t off = 0;
       if (slots >= 0)
         off = ((((int64_t)slots * c.num_kv_heads + kvh) << shift) + (t & (bs - 1))) * D;
 #pragma unroll
@@ -674,7 +676,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
         const uint4 *src = reinterpret_cast<const uint4 *>(codes + o + (tr & 15) * D + 16 * c4);
 #pragma unroll
         for (int pl = 0; pl < D / 64; pl++)
-          x[pl * kTr + i] = o >= 0 ? __ldg(src + 4 * pl) : make_uint4(0, 0, 0, 0);
+          x[pl * kTr + i] = __ldg(src + 4 * pl);
       }
     };
     auto put = [&](uint8_t *dst, const uint4 (&x)[kPer]) {
