@@ -262,7 +262,8 @@ cudaError_t launch_b8_append(const kvq_b8_cache &c, const kvq_heads &k, const kv
                              int bf16, int batch, int t_new, const int32_t *start_pos,
                              const int32_t *new_lens, const kvq_rope_spec &spec,
                              const int32_t *rope_pos, cudaStream_t s) {
-  const int cols = min((t_new + c.block_size - 2) / c.block_size + 1, c.max_blocks_per_seq);
+  const int cols = (int)min(((int64_t)t_new + c.block_size - 2) / c.block_size + 1,
+                            (int64_t)c.max_blocks_per_seq);
   const int items = min(t_new, c.block_size) * (c.head_dim / 16);
   int threads = 32;
   while (threads < kThreads && threads < items) threads *= 2;

@@ -70,7 +70,7 @@ cudaError_t launch_rope(const kvq_rope_spec &spec, int bf16, int head_dim, int n
                         cudaStream_t s) {
   if (num_tokens == 0) return cudaSuccess;
   const int per = min(kTokens, max(1, num_tokens / (4 * kNumSMs)));
-  const int ctas = (num_tokens + per - 1) / per;
+  const int ctas = (num_tokens - 1) / per + 1;
   const size_t smem = (size_t)per * (spec.rot_dim / 2) * sizeof(float2);
   if (bf16)
     rope_kernel<true><<<ctas, kThreads, smem, s>>>(spec, head_dim, num_tokens, per, positions,

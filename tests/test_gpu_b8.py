@@ -538,6 +538,29 @@ def test_evict_long_and_equal_weights():
     assert (wide[..., :keep] == 0.25).all() and (wide[..., keep:] == 0).all()
 
 
+def test_evict_nothing():
+    """A batch without a token, of a longest length of 0."""
+    c, _ = filled(95, [0, 0], 2, 64, 16)
+    into, _ = filled(96, [16, 16], 2, 64, 16)
+    before = into.k_codes.clone()
+    ln, kept, mo = kvq.b8_evict(c, into, torch.zeros((2, 2, 0), device="cuda"), ints([0, 0]), 0, 9)
+    assert ln.tolist() == [0, 0] and (kept == -1).all() and (mo == 0).all()
+    assert torch.equal(before, into.k_codes)
+
+
+def test_append_of_a_batch_padded_without_end():
+    """The padded length sets no cost and passes no range: only 3 tokens are there."""
+    k, v = rand(97, 1, 1, 2, 64, dtype=BF16), rand(98, 1, 1, 2, 64, dtype=BF16)
+    a, b = (kvq.B8Cache.contiguous(1, 2, 64, 64, 32) for _ in "ab")
+    most = (1 << 31) - 1
+    kvq.b8_append(a, k.expand(1, most, 2, 64), v.expand(1, most, 2, 64), ints([30]),
+                  new_lens=ints([3]))
+    kvq.b8_append(b, k.expand(1, 3, 2, 64), v.expand(1, 3, 2, 64), ints([30]))
+    assert torch.equal(a.k_codes, b.k_codes) and torch.equal(a.v_codes, b.v_codes)
+    assert torch.equal(a.k_scales, b.k_scales) and torch.equal(a.v_scales, b.v_scales)
+    assert (a.k_scales > 0).any()
+
+
 # ------------------------------------------------------------------ as used
 def test_large_planes():
     """Blocks beyond 2^32 bytes of a plane."""
