@@ -12,7 +12,7 @@
 //
 // Prompts of 8 sequences (197 thousand rows of 256 dims of K and of V, bf16, K
 // rotated, blocks of 64): append 108 us, 303 MB; issue slots 62 % used, the
-// angles a third of them (49 us at a plain copy's rate).  Read back: 62 us, 4.9
+// angles a third of them (49 us at a plain copy's rate).  Read back: 51 us, 5.9
 // TB/s, two thirds of it stores.  One token in each of 64 sequences: 5.5 us and
 // 4.4 us, launches and chains of dependent loads.
 #include "b8_common.cuh"
@@ -193,53 +193,78 @@ __global__ void __launch_bounds__(kThreads, 3)
   if (threadIdx.x == 0) *scale_at = scale;
 }
 
-// grid: (run of kN x 256 pieces of a sequence's rows, sequence).  A piece is 8
-// elements of K and of V: adjacent threads store adjacent 16 (bf16) or 32
-// bytes, and all of a thread's codes and scales are on their way before the
-// first is used.
-template <bool BF16, int D, int kN>
+// 32 bytes to `at`; wide: it is 32-byte aligned
+__device__ __forceinline__ void store32(void *at, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    uint4 *p = static_cast<uint4 *>(at);
+    p[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+// 16 codes as values at element `elem`
+template <bool BF16>
+__device__ __forceinline__ void decode16(void *base, int64_t elem, const uint4 &codes, float scale,
+                                         bool wide) {
+  float x[16];
+  b8::decode4(codes.x, scale, x), b8::decode4(codes.y, scale, x + 4);
+  b8::decode4(codes.z, scale, x + 8), b8::decode4(codes.w, scale, x + 12);
+  uint32_t w[8];
+  if (BF16) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    store32(static_cast<uint16_t *>(base) + elem, w, wide);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) w[i] = __float_as_uint(x[8 * h + i]);
+      store32(static_cast<float *>(base) + elem + 8 * h, w, wide);
+    }
+  }
+}
+
+// grid: (run of 256 pieces of a sequence's rows, sequence).  A piece is 16
+// elements of K and of V, stored 32 bytes at a time where the outputs are
+// aligned to that: 134 MB of codes to 268 MB of bf16 take 60 us, two 16-byte
+// stores a piece 78.
+template <bool BF16, int D>
 __global__ void __launch_bounds__(kThreads)
     b8_gather_kernel(kvq_b8_cache c, uint32_t total, int count,
                      const int32_t *__restrict__ first, const int32_t *__restrict__ ends,
-                     void *__restrict__ k_out, void *__restrict__ v_out,
+                     void *__restrict__ k_out, void *__restrict__ v_out, bool wide,
                      uint32_t *__restrict__ err) {
-  constexpr uint32_t kPieces = D / 8;
+  constexpr uint32_t kPieces = D / 16;
   const int b = blockIdx.y;
   const uint32_t hkv = c.num_kv_heads;
   const int shift = __ffs(c.block_size) - 1;
   const int64_t t0 = __ldg(first + b);
   const int64_t cap = min((int64_t)__ldg(ends + b), (int64_t)c.max_blocks_per_seq * c.block_size);
-  uint2 kw[kN], vw[kN];
-  float ks[kN], vs[kN];
-  const uint32_t i0 = blockIdx.x * (kN * kThreads) + threadIdx.x;
-#pragma unroll
-  for (int n = 0; n < kN; n++) {
-    const uint32_t i = i0 + n * kThreads;
-    kw[n] = vw[n] = make_uint2(0, 0);
-    ks[n] = vs[n] = 0.f;
-    const uint32_t row = i / kPieces, tok = row / hkv, h = row - tok * hkv;
-    const int64_t t = t0 + tok;
-    int64_t slot = -1;
-    if (i < total && t >= 0 && t < cap) slot = b8::block_of(c, b, (int)(t >> shift));
-    if (slot < 0 || !in_bounds(slot, slot + 1, c.num_blocks, err)) continue;
+  const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+  if (i >= total) return;
+  const uint32_t row = i / kPieces, tok = row / hkv, h = row - tok * hkv;
+  const int64_t t = t0 + tok;
+  int64_t slot = -1;
+  if (t >= 0 && t < cap) slot = b8::block_of(c, b, (int)(t >> shift));
+  uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
+  float ks = 0.f, vs = 0.f;
+  if (slot >= 0 && in_bounds(slot, slot + 1, c.num_blocks, err)) {
     const int64_t sh = slot * hkv + h;
-    const int64_t at = ((sh << shift) + (t & (c.block_size - 1))) * D + 8 * (i % kPieces);
-    kw[n] = __ldg(reinterpret_cast<const uint2 *>(c.k_codes + at));
-    vw[n] = __ldg(reinterpret_cast<const uint2 *>(c.v_codes + at));
-    ks[n] = __ldg(c.k_scales + sh);
-    vs[n] = __ldg(c.v_scales + sh);
+    const int64_t at = ((sh << shift) + (t & (c.block_size - 1))) * D + 16 * (i % kPieces);
+    kw = __ldg(reinterpret_cast<const uint4 *>(c.k_codes + at));
+    vw = __ldg(reinterpret_cast<const uint4 *>(c.v_codes + at));
+    ks = __ldg(c.k_scales + sh);
+    vs = __ldg(c.v_scales + sh);
   }
-#pragma unroll
-  for (int n = 0; n < kN; n++) {
-    const uint32_t i = i0 + n * kThreads;
-    if (i >= total) break;
-    const int64_t to = ((int64_t)b * total + i) * 8;
-    float x[8];
-    b8::decode4(kw[n].x, ks[n], x), b8::decode4(kw[n].y, ks[n], x + 4);
-    store8<BF16>(k_out, to, x);
-    b8::decode4(vw[n].x, vs[n], x), b8::decode4(vw[n].y, vs[n], x + 4);
-    store8<BF16>(v_out, to, x);
-  }
+  const int64_t to = ((int64_t)b * total + i) * 16;
+  decode16<BF16>(k_out, to, kw, ks, wide);
+  decode16<BF16>(v_out, to, vw, vs, wide);
 }
 
 }  // namespace
@@ -280,18 +305,11 @@ cudaError_t launch_b8_append(const kvq_b8_cache &c, const kvq_heads &k, const kv
 template <bool BF16, int D>
 static void gather(const kvq_b8_cache &c, int batch, const int32_t *first, const int32_t *ends,
                    int count, void *k_out, void *v_out, cudaStream_t s) {
-  uint32_t *err = device_error_word();
-  const uint32_t total = (uint32_t)count * c.num_kv_heads * (D / 8);
-  // four pieces a thread once one a thread would fill the card
-  if ((int64_t)total * batch > (int64_t)kNumSMs * 2048) {
-    const dim3 grid((total + 4 * kThreads - 1) / (4 * kThreads), batch);
-    b8_gather_kernel<BF16, D, 4>
-        <<<grid, kThreads, 0, s>>>(c, total, count, first, ends, k_out, v_out, err);
-  } else {
-    const dim3 grid((total + kThreads - 1) / kThreads, batch);
-    b8_gather_kernel<BF16, D, 1>
-        <<<grid, kThreads, 0, s>>>(c, total, count, first, ends, k_out, v_out, err);
-  }
+  const uint32_t total = (uint32_t)count * c.num_kv_heads * (D / 16);
+  const bool wide = (reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) % 32 == 0;
+  const dim3 grid((total + kThreads - 1) / kThreads, batch);
+  b8_gather_kernel<BF16, D><<<grid, kThreads, 0, s>>>(c, total, count, first, ends, k_out, v_out, wide,
+                                                      device_error_word());
 }
 
 cudaError_t launch_b8_gather(const kvq_b8_cache &c, int batch, const int32_t *first,

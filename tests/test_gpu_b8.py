@@ -223,6 +223,19 @@ def test_append_skips_unmapped_blocks_and_tails():
     assert not gk.any()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gather_into_16_byte_alignment(dtype):
+    c, _ = filled(61, [50, 70], 2, 128, 32)
+    first, ends = ints([3, 0]), ints([50, 66])
+    want = kvq.b8_gather(c, first, ends, 67, dtype)
+    size, off = want[0].numel(), 16 // dtype.itemsize
+    got = [torch.full((size + 2 * off,), -7.0, dtype=dtype, device="cuda") for _ in "kv"]
+    views = [x[off:off + size].view(want[0].shape) for x in got]
+    kvq.b8_gather(c, first, ends, 67, dtype, k_out=views[0], v_out=views[1])
+    for w, v, x in zip(want, views, got):
+        assert torch.equal(w, v) and (x[:off] == -7).all() and (x[-off:] == -7).all()
+
+
 # ------------------------------------------------------------------ attention
 def tolerance(dtype, dim, tokens, a, want, vmax):
     """Scores: q keeps 22 bits (bf16: all), each of the dim / 16 (twice that for
