@@ -9,10 +9,12 @@
 // the kept indices where a prefix sum puts them.  Requantization: a warp
 // or a CTA per kept block of a head; rows are held in registers between the
 // block's maximum and the rounding, so kept codes are read once.  Bound: HBM.
-// 16 sequences of 12000 to 16384 tokens to 4096, 8 kv heads, D 128: selection 24
-// us (up to 64 KB of weights a CTA, five walks), requantization 66 us for 268 MB,
+// 16 sequences of 12000 to 16384 tokens to 4096, 8 kv heads, D 128: selection 20
+// us (up to 64 KB of weights a CTA, five walks; instructions), requantization 66 us for 268 MB,
 // 4.1 TB/s, packed fp32 (72 us by single instructions, 8 a code: both products
 // are rounded as an append's).
+#include <type_traits>
+
 #include "b8_common.cuh"
 #include "b8_internal.cuh"
 
@@ -75,83 +77,95 @@ __global__ void __launch_bounds__(kSelThreads)
 #pragma unroll 8
   for (int i = tid; i < nc; i += kSelThreads) keys[i] = order_key(w[i]);
   __syncthreads();
-  auto key_of = [&](int i) { return i < nc ? keys[i] : order_key(w[i]); };
+  // all: every key lies in shared memory
+  auto select = [&](auto all) {
+    auto key_of = [&](int i) { return decltype(all)::value || i < nc ? keys[i] : order_key(w[i]); };
 
-  // the k-th largest key `prefix`, and how many of its equals stay
-  uint32_t prefix = 0, mask = 0;
-  int need = k;
-  if (k > 0) {
+    // the k-th largest key `prefix`, and how many of its equals stay
+    uint32_t prefix = 0, mask = 0;
+    int need = k;
+    if (k > 0) {
 #pragma unroll
-    for (int pass = 0; pass < 3; pass++) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const int nb = pass == 2 ? 1024 : 2048;
-      for (int i = tid; i < nb; i += kSelThreads) bins[i] = 0;
-      __syncthreads();
+      for (int pass = 0; pass < 3; pass++) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const int nb = pass == 2 ? 1024 : 2048;
+        for (int i = tid; i < nb; i += kSelThreads) bins[i] = 0;
+        __syncthreads();
 #pragma unroll 8
-      for (int i = lo + tid; i < hi; i += kSelThreads) {
-        const uint32_t key = key_of(i);
-        if ((key & mask) == prefix) atomicAdd(&bins[key >> shift & (nb - 1)], 1);
-      }
-      __syncthreads();
-      // elements in bins above each: thread t owns the bins of rank 2 t and
-      // 2 t + 1 from the top (one bin in the last pass)
-      const int per = nb / kSelThreads;
-      const int top = nb - 1 - tid * per;
-      const int c0 = bins[top], c1 = per == 2 ? bins[top - 1] : 0;
-      int incl = c0 + c1;
+        for (int i = lo + tid; i < hi; i += kSelThreads) {
+          const uint32_t key = key_of(i);
+          if ((key & mask) == prefix) atomicAdd(&bins[key >> shift & (nb - 1)], 1);
+        }
+        __syncthreads();
+        // elements in bins above each: thread t owns the bins of rank 2 t and
+        // 2 t + 1 from the top (one bin in the last pass)
+        const int per = nb / kSelThreads;
+        const int top = nb - 1 - tid * per;
+        const int c0 = bins[top], c1 = per == 2 ? bins[top - 1] : 0;
+        int incl = c0 + c1;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        if (lane == 31) wsum[0][warp] = incl;
+        __syncthreads();
+        // the warps before this one (as many as a warp has lanes)
+        const int before = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[0][lane] : 0);
+        const int above = before + incl - c0 - c1;
+        if (above < need && need <= above + c0) found[0] = top, found[1] = above;
+        if (above + c0 < need && need <= above + c0 + c1) found[0] = top - 1, found[1] = above + c0;
+        __syncthreads();
+        prefix |= (uint32_t)found[0] << shift;
+        mask |= (uint32_t)(nb - 1) << shift;
+        need -= found[1];
+        __syncthreads();
       }
-      if (lane == 31) wsum[0][warp] = incl;
-      __syncthreads();
-      int above = incl - c0 - c1;
-      for (int i = 0; i < warp; i++) above += wsum[0][i];
-      if (above < need && need <= above + c0) found[0] = top, found[1] = above;
-      if (above + c0 < need && need <= above + c0 + c1) found[0] = top - 1, found[1] = above + c0;
-      __syncthreads();
-      prefix |= (uint32_t)found[0] << shift;
-      mask |= (uint32_t)(nb - 1) << shift;
-      need -= found[1];
-      __syncthreads();
     }
-  }
-  // in order: warp v takes a run of tokens, 32 at a time
-  const int run = (n + kWarps * 32 - 1) / (kWarps * 32) * 32;
-  const int r0 = min(n, warp * run), r1 = min(n, r0 + run);
-  auto kind = [&](int i) {  // 2: kept, 1: equal to the border, 0: dropped
-    if (i >= r1) return 0;
-    if (i < lo || i >= hi) return 2;
-    if (k == 0) return 0;
-    const uint32_t key = key_of(i);
-    return key > prefix ? 2 : key == prefix ? 1 : 0;
+    // in order: warp v takes a run of tokens, 32 at a time
+    const int run = (n + kWarps * 32 - 1) / (kWarps * 32) * 32;
+    const int r0 = min(n, warp * run), r1 = min(n, r0 + run);
+    // is token i kept for certain; does it equal the border
+    auto kind = [&](int i, bool &over, bool &equal) {
+      const uint32_t key = i < r1 ? key_of(i) : 0u;
+      const bool free = i >= lo && i < hi;
+      over = i < r1 && (!free || (k > 0 && key > prefix));
+      equal = i < r1 && free && k > 0 && key == prefix;
+    };
+    int over = 0, equal = 0;
+#pragma unroll 4
+    for (int i = r0 + lane; i < r1; i += 32) {
+      bool o, e;
+      kind(i, o, e);
+      over += o;
+      equal += e;
+    }
+    over = __reduce_add_sync(0xffffffffu, over);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane == 0) wsum[0][warp] = over, wsum[1][warp] = equal;
+    __syncthreads();
+    over = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[0][lane] : 0);
+    equal = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[1][lane] : 0);
+    const uint32_t below = (1u << lane) - 1;
+#pragma unroll 4
+    for (int i = r0; i < r1; i += 32) {
+      bool is_over, is_equal;
+      kind(i + lane, is_over, is_equal);
+      const uint32_t o = __ballot_sync(0xffffffffu, is_over), e = __ballot_sync(0xffffffffu, is_equal);
+      const int eq = equal + __popc(e & below);  // equals before this token
+      const int at = over + __popc(o & below) + min(eq, need);
+      if (is_over || (is_equal && eq < need)) {
+        kept[at] = i + lane;
+        mout[at] = w[i + lane];
+      }
+      over += __popc(o);
+      equal += __popc(e);
+    }
   };
-  int over = 0, equal = 0;
-#pragma unroll 4
-  for (int i = r0; i < r1; i += 32) {
-    const int x = kind(i + lane);
-    over += __popc(__ballot_sync(0xffffffffu, x == 2));
-    equal += __popc(__ballot_sync(0xffffffffu, x == 1));
-  }
-  if (lane == 0) wsum[0][warp] = over, wsum[1][warp] = equal;
-  __syncthreads();
-  over = equal = 0;
-  for (int i = 0; i < warp; i++) over += wsum[0][i], equal += wsum[1][i];
-  const uint32_t below = (1u << lane) - 1;
-#pragma unroll 4
-  for (int i = r0; i < r1; i += 32) {
-    const int x = kind(i + lane);
-    const uint32_t o = __ballot_sync(0xffffffffu, x == 2), e = __ballot_sync(0xffffffffu, x == 1);
-    const int eq = equal + __popc(e & below);  // equals before this token
-    const int at = over + __popc(o & below) + min(eq, need);
-    if (x == 2 || (x == 1 && eq < need)) {
-      kept[at] = i + lane;
-      mout[at] = w[i + lane];
-    }
-    over += __popc(o);
-    equal += __popc(e);
-  }
+  if (n <= nc)
+    select(std::true_type());
+  else
+    select(std::false_type());
 }
 
 // A block of a head is 1 to 16 runs of 4 KB a plane; one warp holds its run of
