@@ -9,8 +9,9 @@
 // tokens, which then come from L2.  Bound for a few rows: the K codes from HBM.
 // 32 sequences of 2048 to 16384 tokens, 8 kv heads, D 128, one query each: 69
 // us, 4.6 TB/s (71 % of a plain copy; issue slots 51 % used, uneven ends).  The
-// last 32 queries of 4 prompts (128 rows): 38 us, a fourth of it the staging of
-// the rows, the rest latency at 16 warps an SM.
+// last 32 queries of 4 prompts (128 rows): 37 us, a fourth of it the staging of
+// the rows, the rest latency at 16 warps an SM (40 us with 16 tokens a step, whose
+// query fragments are read from shared memory twice as often).
 #include "b8_mma.cuh"
 
 namespace kvq {
@@ -23,13 +24,14 @@ constexpr int kThreads = 32 * kWarps;
 
 template <int D, int R, bool BF16>
 struct Cfg {
-  static constexpr int kTiles = D == 256 || R == 16 ? 1 : 2;  // 16-token tiles of a warp's step
-  static constexpr int kTileBytes = kTok * D;
-  static constexpr int kStageBytes = kTiles * (kTileBytes + 16);  // + k_scale
-  static constexpr int kStages = 3;  // 128 KB in flight or landing per SM
-  static constexpr int kChunk = R == 8 ? 8 : 128;   // rows staged at once
   // many bf16 rows: fp16 products, K codes converted once for all of them
   static constexpr bool kHalf = R == 16 && BF16;
+  // 16-token tiles of a warp's step
+  static constexpr int kTiles = D == 256 || (R == 16 && !kHalf) ? 1 : 2;
+  static constexpr int kTileBytes = kTok * D;
+  static constexpr int kStageBytes = kTiles * (kTileBytes + 16);  // + k_scale
+  static constexpr int kStages = kHalf && kTiles == 2 ? 2 : 3;  // 64 to 128 KB in flight an SM
+  static constexpr int kChunk = R == 8 ? 8 : 128;   // rows staged at once
   static constexpr int kQWords = kHalf ? HTile<D>::kWords : QTile<D, R, BF16>::kWords;
   static constexpr int kOffInv = kWarps * kStages * kStageBytes;
   static constexpr int kOffLse = kOffInv + kChunk * 4;
@@ -311,7 +313,7 @@ cudaError_t launch_b8_mass(const kvq_b8_cache &c, const B8Queries &q, const floa
   const int64_t len =
       max((int64_t)1, min((int64_t)q.max_seq_len, (int64_t)c.max_blocks_per_seq * c.block_size));
   const bool few = (int64_t)q.max_q * q.group <= 8;
-  const int64_t granule = kWarps * kTok * (c.head_dim == 256 || !few ? 1 : 2);
+  const int64_t granule = kWarps * kTok * (c.head_dim == 256 || (!few && !q.bf16) ? 1 : 2);
   const int64_t units = (int64_t)q.batch * c.num_kv_heads;
   const int64_t most = (len + granule - 1) / granule;
   const int64_t resident = kNumSMs * 2;
