@@ -757,36 +757,35 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
     // ---------------------------------------------------------- issue
     constexpr uint32_t kIdS = instr_desc(kBN, false), kIdO = instr_desc(D, true);
     bool ok = true;
+    // descriptors of the operands' first pieces; a piece `bytes` on adds bytes / 16
+    const uint64_t q0d = smem_desc(base, 16, 1024), k0d = smem_desc(base + C::kOffK, 16, 1024),
+                   v0d = smem_desc(base + C::kOffV, kBN * 128, 1024);
     auto issue_s = [&](int i) {
-      const int j = i / nt, t = i - j * nt, st = j & 1;
+      const int j = nt == 2 ? i >> 1 : i, t = i - j * nt, st = j & 1;
       if (t == 0) ok = wait1(k_full + 8 * st, (j >> 1) & 1);
       if (!ok) return;
       t5_after();
       const uint32_t d = tmem + C::kColS + (i & 1) * kBN;
+      const uint64_t qd = q0d + (t ? C::kQTileBytes / 16 : 0), kd = k0d + (st ? C::kKVBytes / 16 : 0);
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ks++) {
-        const uint32_t at = (ks & 3) * 32;
-        const uint64_t qa = smem_desc(base + t * C::kQTileBytes + (ks >> 2) * (128 * 128) + at, 16, 1024);
-        const uint64_t kb =
-            smem_desc(base + C::kOffK + st * C::kKVBytes + (ks >> 2) * (kBN * 128) + at, 16, 1024);
-        t5_mma_ss(d, qa, kb, kIdS, ks > 0);
-      }
+      for (int ks = 0; ks < D / 16; ks++)
+        t5_mma_ss(d, qd + ((ks >> 2) * (128 * 128) + (ks & 3) * 32) / 16,
+                  kd + ((ks >> 2) * (kBN * 128) + (ks & 3) * 32) / 16, kIdS, ks > 0);
       t5_commit(s_full + 8 * (i & 1));
       if (t == nt - 1) t5_commit(k_empty + 8 * st);
     };
     for (int i = 0; i < min(2, n_items) && ok; i++) issue_s(i);
     for (int i = 0; i < n_items && ok; i++) {
-      const int j = i / nt, t = i - j * nt, st = j & 1;
+      const int j = nt == 2 ? i >> 1 : i, t = i - j * nt, st = j & 1;
       ok = wait1(p_full + 8 * (i & 1), (i >> 1) & 1);
       if (ok && t == 0) ok = wait1(v_full + 8 * st, (j >> 1) & 1);
       if (!ok) break;
       t5_after();
       const uint32_t p = tmem + C::kColS + (i & 1) * kBN;
+      const uint64_t vd = v0d + (st ? C::kKVBytes / 16 : 0);
 #pragma unroll
-      for (int ks = 0; ks < kBN / 16; ks++) {
-        const uint64_t vb = smem_desc(base + C::kOffV + st * C::kKVBytes + ks * 2048, kBN * 128, 1024);
-        t5_mma_ts(tmem + C::kColO + t * D, p + 8 * ks, vb, kIdO, j > 0 || ks > 0);
-      }
+      for (int ks = 0; ks < kBN / 16; ks++)
+        t5_mma_ts(tmem + C::kColO + t * D, p + 8 * ks, vd + ks * (2048 / 16), kIdO, j > 0 || ks > 0);
       t5_commit((j == n_tiles - 1 ? all_done : o_done) + 8 * t);
       if (t == nt - 1) t5_commit(v_empty + 8 * st);
       if (i + 2 < n_items) issue_s(i + 2);
