@@ -513,7 +513,8 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoft));
     if (soft) {
     // ---------------------------------------------------------- softmax
-    const int lim = live ? max(0, len - nq + qi + 1) : 0;
+    // (rows of no query: all tokens, so that they cost their warp no masks)
+    const int lim = live ? max(0, len - nq + qi + 1) : 1 << 30;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // 32 lanes a warp
     const uint32_t o_at = lanes + C::kColO + wg * D;
     float m = -1e30f, l = 0.f, vref = 0x1p-100f;
@@ -777,8 +778,9 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
     for (int i = 0; i < min(2, n_items) && ok; i++) issue_s(i);
     for (int i = 0; i < n_items && ok; i++) {
       const int j = nt == 2 ? i >> 1 : i, t = i - j * nt, st = j & 1;
-      ok = wait1(p_full + 8 * (i & 1), (i >> 1) & 1);
-      if (ok && t == 0) ok = wait1(v_full + 8 * st, (j >> 1) & 1);
+      // V first: it has long been there when the probabilities come
+      if (t == 0) ok = wait1(v_full + 8 * st, (j >> 1) & 1);
+      ok = ok && wait1(p_full + 8 * (i & 1), (i >> 1) & 1);
       if (!ok) break;
       t5_after();
       const uint32_t p = tmem + C::kColS + (i & 1) * kBN;
