@@ -20,11 +20,15 @@
 // maximum has a slack of 8, so O is rarely rescaled (by its softmax threads).
 // Bound: the chain scores -> softmax -> products of a row tile; two tiles take
 // turns on the tensor pipe.  4 prompts of 572 to 778 queries, 32 heads on 8 kv
-// heads, D 128, 6516 to 8075 tokens: 410 us, 748 TFLOP/s (46 % of a cuBLAS bf16
-// product; the pipe is busy 37 % of the cycles).  Without exp2, or without the
-// stores of P, it takes as long; with next to no softmax 354 us, with half of the
-// score products 383.  Tiles of 64 tokens with two score buffers a row tile took
-// 660 us (their products cost as much as those of 128), P in halves 560.
+// heads, D 128, 6516 to 8075 tokens: 385 us, 795 TFLOP/s (48 % of a cuBLAS bf16
+// product).  A tile's 16 products take about 2000 cycles from the first to the
+// last where their operations are 1024, V's layout (dims as rows or as columns)
+// aside; descriptors by constant steps, the wait for V in front of that for the
+// probabilities and no masks for rows of no query brought 410 to 385.  At 410 it
+// took as long without exp2, or without the stores of P; 354 with next to no
+// softmax, 383 with half of the score products, 379 without the conversion.
+// Tiles of 64 tokens with two score buffers a row tile took 660 us (their
+// products cost as much as those of 128), P in halves 560.
 #include <cuda_bf16.h>
 
 #include "b8_attn.cuh"
