@@ -238,7 +238,8 @@ kvq_status kvq_b8_evict(const kvq_b8_cache *src, const kvq_b8_cache *dst, int32_
       keep > (int64_t)dst->max_blocks_per_seq * dst->block_size)
     return KVQ_ERR_INVALID_ARG;
   if (batch == 0) return KVQ_OK;
-  if (!d_seq_lens || (!mass && max_seq_len > 0) || !new_lens || !kept || !mass_out || mass_stride < max_seq_len ||
+  if (!d_seq_lens || new_lens == d_seq_lens || (!mass && max_seq_len > 0) || !new_lens || !kept ||
+      !mass_out || mass_out == mass || mass_stride < max_seq_len ||
       mass_out_stride < keep)
     return KVQ_ERR_INVALID_ARG;
   if (2LL * batch * src->num_kv_heads >= (1LL << 31) / (keep / dst->block_size + 1))

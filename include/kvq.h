@@ -576,7 +576,7 @@ KVQ_API kvq_status kvq_b8_attn_mass(const kvq_b8_cache *cache, const kvq_b8_quer
  *   or another cache.  Blocks of dst must be no blocks of src that the call
  *   reads, and dst's table must hold keep tokens a sequence.
  *   mass: device fp32 [batch][num_kv_heads][mass_stride].
- *   new_lens: device int32[batch], min(n, keep);
+ *   new_lens: device int32[batch], not d_seq_lens itself: min(n, keep);
  *   kept: device int32[batch][num_kv_heads][keep], the kept tokens' old
  *   indices, -1 behind the last;
  *   mass_out: device fp32 [batch][num_kv_heads][mass_out_stride], not

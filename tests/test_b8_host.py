@@ -195,6 +195,21 @@ def test_mass_and_evict_refusals(L, p16):
         assert evict(**kw) == INVALID, kw
 
 
+def test_evict_outputs_are_no_inputs(L, p16):
+    """Each refusal alone: pointers that differ, then one shared."""
+    d = cache_desc(p16)
+    at = {n: C.c_void_p((i + 2) * 4096) for i, n in enumerate(("lens", "mass", "new", "kept", "out"))}
+
+    def evict(ms=64, mo=8, **kw):
+        p = {**at, **kw}
+        return L.kvq_b8_evict(C.byref(d), C.byref(d), 1, p["lens"], 64, p["mass"], ms, 8, 2, 2,
+                              p["new"], p["kept"], p["out"], mo, None)
+
+    for kw in (dict(new=at["lens"]), dict(out=at["mass"]), dict(mass=None), dict(lens=None),
+               dict(new=None), dict(kept=None), dict(out=None), dict(ms=63), dict(mo=7)):
+        assert evict(**kw) == INVALID, kw
+
+
 def test_bindings_check_shapes_first():
     z = lambda *s, t=torch.float32: torch.zeros(s, dtype=t)
     with pytest.raises(ValueError, match="codes"):
