@@ -796,12 +796,12 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       if (t == nt - 1) t5_commit(v_empty + 8 * st);
       if (i + 2 < n_items) issue_s(i + 2);
     }
-    if (!ok) {
-      // products may be in flight: they end before tensor memory is given back
-      // (a bounded wait, like every other)
-      t5_commit(drain);
-      for (int n = 0; n < (1 << 20) && !dec::mbar_try(drain, 0); n++) {
-      }
+    // Products end before tensor memory is given back and the CTA leaves, whoever
+    // gave up: a softmax warp may have done so after the last product's issue.  (A
+    // bounded wait, like every other.  It covers the commits to k_empty and v_empty
+    // that nobody waits for, too.)
+    t5_commit(drain);
+    for (int n = 0; n < (1 << 20) && !dec::mbar_try(drain, 0); n++) {
     }
     }
   }

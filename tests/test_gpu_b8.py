@@ -477,6 +477,37 @@ def test_wait_timeout_is_reported_and_recovers():
     assert torch.equal(again, want)
 
 
+def test_waits_that_run_out_at_any_place():
+    """Limits that let a wait of any role run out, early, late or never: a row is
+    NaN or exact, NaN comes with the flag, and calls beside and after it, which
+    may take over its multiprocessors' memory, are exact."""
+    c, _ = filled(87, [2500, 700], 2, 128, 64)
+    q = rand(88, 300, 8, 128, dtype=BF16)
+    args = (c, q, ints([2500, 700]), 2500, 0.08)
+    kw = dict(cu_q=ints([0, 200, 300]), max_q=200, return_lse=True)
+    want, wlse = kvq.b8_attn(*args, **kw)
+    assert kvq.device_errors() == 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for polls in list(range(12)) + [16, 24, 40, 80, 200]:
+        kvq.set_wait_limit(polls)
+        try:
+            got = [kvq.b8_attn(*args, **kw) for _ in range(3)]
+        finally:
+            kvq.set_wait_limit(-1)
+        after = [kvq.b8_attn(*args, **kw), kvq.b8_attn(*args, stream=side, **kw)]
+        flags = kvq.device_errors()  # synchronises
+        bad = False
+        for out, lse in got:
+            nan = torch.isnan(lse)
+            assert torch.equal(out[~nan], want[~nan]) and torch.equal(lse[~nan], wlse[~nan])
+            assert torch.isnan(out[nan]).all()
+            bad |= bool(nan.any())
+        assert not bad or flags == kvq.KVQ_DEVERR_WAIT_TIMEOUT
+        for out, lse in after:
+            assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
 def test_bad_query_ranges_have_no_queries():
     c, _ = filled(81, [50, 50, 50], 1, 64, 16)
     q = rand(82, 12, 2, 64)
