@@ -15,10 +15,12 @@
 // on short batches: not taken.
 //   * Scores are kept in log2 units in fp32; m follows the row maximum with a
 //     slack of 8 (p up to 2^8), so O is rarely rescaled.
-//   * P enters the second product as p * v_scale / vref in fp16 (bf16 output)
-//     or as fp16 hi + lo (fp32 output), where vref is the warp's largest
-//     power-of-two bound of the block scales so far and 64 / vref keeps the
-//     products at most 2^14; l sums the unrounded p.
+//   * P enters the second product as p * v_scale in fp16 (bf16 output) or as
+//     fp16 hi + lo (fp32 output), in units of 2^mv / 64 where mv follows the
+//     row's maximum of score + log2(v_scale) as m does that of the scores: at
+//     most 2^14, and fp16's range counts down from the row's own largest p *
+//     v_scale, whatever scales its other tokens have.  l sums the unrounded p.
+//     m and mv are integers, so factors between them are powers of two.
 #include <cuda_bf16.h>
 
 #include "b8_attn.cuh"
@@ -48,11 +50,11 @@ struct Cfg {
   static constexpr int kOffInv = kOffQ + QTile<D, R, !HILO>::kBytes;
   static constexpr int kOffLim = kOffInv + R * 4;
   static constexpr int kSmem = kOffLim + R * 4;
-  // the merge reuses the ring: per warp R x (D + 4) of O, then m, l and vref
+  // the merge reuses the ring: per warp R x (D + 4) of O, then m, l and mv
   static constexpr int kRow = D + 4;
   static constexpr int kOffM = kWarps * R * kRow * 4;
   // in a cluster: this CTA's merged record, read by the others
-  static constexpr int kOffRec = (kOffM + kWarps * (2 * R + 1) * 4 + 15) / 16 * 16;
+  static constexpr int kOffRec = (kOffM + kWarps * 3 * R * 4 + 15) / 16 * 16;
   static_assert(kOffRec + R * kRow * 4 <= kRing, "merge fits the ring");
   static_assert(kSmem * kCtas <= 227 * 1024, "shared memory per SM");
 };
@@ -202,10 +204,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
     for (int n = 0; n < kNb; n++)
 #pragma unroll
       for (int e = 0; e < 4; e++) o[j][n][e] = 0.f;
-  float m[kNb], l[kNb];
+  // vinv: 64 * 2^(m - mv)
+  float m[kNb], l[kNb], mv[kNb], vinv[kNb];
 #pragma unroll
-  for (int n = 0; n < kNb; n++) m[n] = kEmpty, l[n] = 0.f;
-  float vref = 0x1p-100f, vinv = 0x1p106f;  // vinv: 64 / vref
+  for (int n = 0; n < kNb; n++) m[n] = mv[n] = kEmpty, l[n] = 0.f, vinv[n] = 1.f;
   // rows of the V matrices that this lane addresses
   const int v_row = (lane & 7) + (lane & 8), v_ch = lane >> 4;
 
@@ -265,33 +267,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
         for (int e = 0; e < 4; e++)
           if (tok + 8 * (e >> 1) + 2 * tg + (e & 1) >= (nb ? lim1 : lim0)) p[nb][e] = -INFINITY;
     }
-    // m need not be the maximum: it moves once a score passes it by kSlack
-    const bool vgrow = kv.y > vref;
-    bool grow = vgrow;
+    // m and mv need not be the maxima: they move once those pass them by kSlack
+    const float lv = __log2f(kv.y);  // -inf for a block of zeros
+    bool grow = false;
 #pragma unroll
-    for (int nb = 0; nb < kNb; nb++)
-      grow |= fmaxf(fmaxf(p[nb][0], p[nb][1]), fmaxf(p[nb][2], p[nb][3])) > m[nb] + kSlack;
+    for (int nb = 0; nb < kNb; nb++) {
+      const float x = fmaxf(fmaxf(p[nb][0], p[nb][1]), fmaxf(p[nb][2], p[nb][3]));
+      grow |= x > m[nb] + kSlack || x + lv > mv[nb] + kSlack;
+    }
     if (__any_sync(0xffffffffu, grow)) {
-      float vfac = 1.f;
-      if (vgrow) {
-        // power of two at or above the scale (infinite scales give NaN)
-        const float nref = __uint_as_float((__float_as_uint(kv.y) + 0x7fffffu) & 0x7f800000u);
-        vfac = __fdiv_rn(vref, nref);
-        vref = nref;
-        vinv = __fdiv_rn(64.f, nref);
-      }
 #pragma unroll
       for (int nb = 0; nb < kNb; nb++) {
         float x = fmaxf(fmaxf(p[nb][0], p[nb][1]), fmaxf(p[nb][2], p[nb][3]));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        const float mn = x > m[nb] + kSlack ? x : m[nb];
-        const float al = ex2(m[nb] - mn);
-        l[nb] *= al;
+        const float mn = x > m[nb] + kSlack ? ceilf(x) : m[nb];
+        l[nb] *= ex2(m[nb] - mn);
         m[nb] = mn;
+        const float vn = x + lv > mv[nb] + kSlack ? ceilf(x + lv) : mv[nb];
+        const float al = ex2(mv[nb] - vn);
+        mv[nb] = vn;
+        // scales down to 2^-107, which an append makes, stay below 2^126
+        vinv[nb] = ex2(fminf(fmaxf(mn - vn + 6.f, -126.f), 126.f));
         // this lane's columns of O are rows 2 tg and 2 tg + 1 of the block
-        const float a0 = __shfl_sync(0xffffffffu, al, 8 * tg) * vfac;
-        const float a1 = __shfl_sync(0xffffffffu, al, 8 * tg + 4) * vfac;
+        const float a0 = __shfl_sync(0xffffffffu, al, 8 * tg);
+        const float a1 = __shfl_sync(0xffffffffu, al, 8 * tg + 4);
 #pragma unroll
         for (int j = 0; j < kMt; j++) {
           o[j][nb][0] *= a0, o[j][nb][1] *= a1;
@@ -299,10 +299,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
         }
       }
     }
-    const float vf = kv.y * vinv;
     uint32_t ph[kNb][2], pl[kNb][2];
 #pragma unroll
     for (int nb = 0; nb < kNb; nb++) {
+      const float vf = kv.y * vinv[nb];
 #pragma unroll
       for (int n = 0; n < 2; n++) {
         const float e0 = ex2(p[nb][2 * n] - m[nb]), e1 = ex2(p[nb][2 * n + 1] - m[nb]);
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
   // ---- merge of the warps' states
   float *mo = reinterpret_cast<float *>(smem) + warp * R * C::kRow;
   float *mm = reinterpret_cast<float *>(smem + C::kOffM);  // [warp][R]
-  float *ml = mm + kWarps * R, *mv = ml + kWarps * R;
+  float *ml = mm + kWarps * R, *mvs = ml + kWarps * R;
 #pragma unroll
   for (int nb = 0; nb < kNb; nb++) {
 #pragma unroll
@@ -356,9 +356,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
     if (tg == 0) {
       mm[warp * R + 8 * nb + g] = m[nb];
       ml[warp * R + 8 * nb + g] = l[nb];
+      mvs[warp * R + 8 * nb + g] = mv[nb];
     }
   }
-  if (lane == 0) mv[warp] = vref * 0x1p-6f;
   __syncthreads();
   // warp w: rows w, w + 8
   for (int r = warp; r < R; r += kWarps) {
@@ -370,9 +370,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
     float f[kWarps];
 #pragma unroll
     for (int w = 0; w < kWarps; w++) {
-      f[w] = ex2(mm[w * R + r] - M);
-      L += f[w] * ml[w * R + r];
-      f[w] *= mv[w];
+      L += ex2(mm[w * R + r] - M) * ml[w * R + r];
+      f[w] = ex2(mvs[w * R + r] - M - 6.f);
     }
     const bool direct = a.p.splits == 1;
     const float norm = direct ? (L > 0.f ? __fdiv_rn(1.f, L) : L == 0.f ? 0.f : L) : 1.f;

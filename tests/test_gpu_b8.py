@@ -392,6 +392,56 @@ def test_wide_ranges_of_values(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("nq", [1, 3])
+@pytest.mark.parametrize("span", [10, 30, 60])
+@pytest.mark.parametrize("lean", [0.0, 0.5, 1.0, 2.0])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_blocks_of_far_scales(dtype, nq, span, lean, zeros):
+    """V block scales from 2^-span to 2^span in any order.  Each token's score is
+    -lean * log(scale): at 2 the weight lies on the smallest scales and the largest
+    ones, seen or masked, add nothing.  The error is counted in what each row's own
+    tokens weigh, not in the cache's largest scale."""
+    dim, block, n = 128, 16, 6000 + 4 * nq  # several tiles a warp
+    c, _ = filled(171, [n], 1, dim, block)
+    cols = c.block_table.shape[1]
+    g = torch.Generator().manual_seed(172)
+    e = torch.linspace(-span, span, cols)[torch.randperm(cols, generator=g)]
+    pages = c.block_table[0].long().cpu()
+    ks, vs, kc = (x.cpu().clone() for x in (c.k_scales, c.v_scales, c.k_codes))
+    ks[pages] = 0.5
+    vs[pages] = torch.exp2(e + torch.rand(cols, generator=g))[:, None]
+    kc[pages] = (kc[pages].float() / 6).round().to(torch.int8)
+    kc[pages, :, :, 0] = (-lean * math.log(2) * e).round().to(torch.int8)[:, None, None]
+    if zeros:  # most of the weight on a block of zeros
+        vs[pages[3]] = 0
+        c.v_codes[pages[3].item()] = 0
+        kc[pages[3], :, :, 0] = kc[pages, 0, 0, 0].max() + 8
+    c.k_scales.copy_(ks), c.v_scales.copy_(vs), c.k_codes.copy_(kc)
+    q = rand(173, nq, 4, dim) / 50
+    q[..., 0] = 2.0
+    q = q.to(dtype)
+    cu = [0, nq]
+    out, lse = kvq.b8_attn(c, q, ints([n]), n, 1.0, cu_q=ints(cu), max_q=nq, return_lse=True)
+    r = ref.Cache(c)
+    want, wlse, a = ref.attention(r, q, [n], cu, 1.0)
+    k, _ = r.values("k", 0, n)
+    v, _ = r.values("v", 0, n)
+    see = torch.arange(n)[None] <= n - nq + torch.arange(nq)[:, None]
+    s = torch.einsum("qhd,td->qht", q.double().cpu(), k[0]).masked_fill(~see[:, None], -math.inf)
+    p = torch.exp(s - wlse[..., None])
+    scale_of = r.scales["v"][r.table[0]].double()[:, 0].repeat_interleave(block)[:n]
+    # P * v_scale: fp16's half step of itself, or of its subnormals, 2^-25, in
+    # units where the row's largest is 2^5 at least (see `tolerance` for the rest)
+    tol, ltol = tolerance(dtype, dim, n, a, want * 0, torch.tensor(1.0))
+    tol = (tol * (p @ v[0].abs())
+           + 2.0 ** -30 * (p * scale_of).amax(-1, keepdim=True) * 127 * n
+           + want.abs() * (2.0 ** -8 if dtype == BF16 else 2.0 ** -24))
+    err = (out.double().cpu() - want).abs()
+    assert (err <= tol).all(), (err / tol).max()
+    assert ((lse.double().cpu() - wlse).abs() <= ltol + wlse.abs() * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("scale", [0.0, -0.125])
 def test_other_scales(dtype, scale):
     c, _ = filled(73, [300, 40], 1, 64, 32)
