@@ -302,7 +302,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
     uint32_t ph[kNb][2], pl[kNb][2];
 #pragma unroll
     for (int nb = 0; nb < kNb; nb++) {
-      const float vf = kv.y * vinv[nb];
+      // (finite: a product past 2^127 would meet weights below 2^-113 alone, and
+      // 0 * inf would be NaN)
+      float vf = kv.y * vinv[nb];
+      vf = vf > 0x1p127f ? 0x1p127f : vf;
 #pragma unroll
       for (int n = 0; n < 2; n++) {
         const float e0 = ex2(p[nb][2 * n] - m[nb]), e1 = ex2(p[nb][2 * n + 1] - m[nb]);

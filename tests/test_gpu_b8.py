@@ -431,14 +431,38 @@ def test_blocks_of_far_scales(dtype, nq, span, lean, zeros):
     p = torch.exp(s - wlse[..., None])
     scale_of = r.scales["v"][r.table[0]].double()[:, 0].repeat_interleave(block)[:n]
     # P * v_scale: fp16's half step of itself, or of its subnormals, 2^-25, in
-    # units where the row's largest is 2^5 at least (see `tolerance` for the rest)
+    # units where the row's largest is 2^5 at least (see `tolerance` for the rest).
+    # Weights below 2^-112 of the row's largest leave fp32's range on the way.
+    gone = torch.where(p < p.amax(-1, keepdim=True) * 2.0 ** -112, p, 0.0)
     tol, ltol = tolerance(dtype, dim, n, a, want * 0, torch.tensor(1.0))
     tol = (tol * (p @ v[0].abs())
            + 2.0 ** -30 * (p * scale_of).amax(-1, keepdim=True) * 127 * n
-           + want.abs() * (2.0 ** -8 if dtype == BF16 else 2.0 ** -24))
+           + gone @ v[0].abs() + want.abs() * (2.0 ** -8 if dtype == BF16 else 2.0 ** -24))
     err = (out.double().cpu() - want).abs()
     assert (err <= tol).all(), (err / tol).max()
     assert ((lse.double().cpu() - wlse).abs() <= ltol + wlse.abs() * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("nq", [1, 40])
+def test_scales_as_far_as_they_go(dtype, nq):
+    """Scales of 2^-107 and 2^100, weights that lean 2^-240 the other way: what
+    fp32 cannot hold counts as nothing, and nothing becomes NaN."""
+    n, block = 4000, 16
+    c, _ = filled(174, [n], 1, 64, block)
+    c.k_codes[..., 0] = 127
+    big = torch.arange(c.num_blocks, device="cuda") % 2 == 1
+    for hi, lo in ((100, -107), (61, -60), (50, -20)):
+        c.v_scales[:] = torch.where(big, 2.0 ** hi, 2.0 ** lo)[:, None]
+        for lean in (-1.2, -1.0, -0.9, 0.9, 1.0):
+            # q . k * scale: 127 * k_scale, natural units
+            c.k_scales[:] = torch.where(big, lean, 0.0)[:, None] * (hi - lo) * math.log(2) / 127
+            c.k_scales.abs_()
+            q = torch.zeros((nq, 1, 64), device="cuda", dtype=dtype)
+            q[..., 0] = math.copysign(1.0, lean)
+            out, lse = kvq.b8_attn(c, q, ints([n]), n, 1.0, cu_q=ints([0, nq]), max_q=nq,
+                                   return_lse=True)
+            assert torch.isfinite(out).all() and torch.isfinite(lse).all()
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
