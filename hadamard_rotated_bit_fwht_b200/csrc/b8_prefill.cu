@@ -14,10 +14,13 @@
 //            its own for the split of the registers).
 // Scores are scaled after the product: a row's factor is its thread's, a
 // block's scale one of 8 group constants of the tile.  The V scale joins the
-// exponent: p' = 2^(s - m + log2(64 v_scale / vref)), where vref is the
-// largest power-of-two bound of the V scales so far, so O is in units of vref / 64;
-// l sums p' of each 16-token group times the inverse of that factor.  The
-// maximum has a slack of 8, so O is rarely rescaled (by its softmax threads).
+// exponent: p' = 2^(s + log2 v_scale - ve), where ve follows the row's maximum of
+// that sum less 6 (p' up to 2^6, and 2^14 with a slack of 8, so that O is rarely
+// rescaled by its softmax threads): fp16's range counts down from the row's own
+// largest p * v_scale.  O is in units of 2^ve, and so is l, which sums p' of each
+// 16-token group divided by v_scale (and 2^20, to stay far from fp32's ends).  V
+// scales 2^-97 and more below the largest so far count as that: fp32 would lose
+// their p' from l.
 // Bound: the chain scores -> softmax -> products of a row tile; two tiles take
 // turns on the tensor pipe.  4 prompts of 572 to 778 queries, 32 heads on 8 kv
 // heads, D 128, 6516 to 8075 tokens: 385 us, 795 TFLOP/s (48 % of a cuBLAS bf16
@@ -59,7 +62,8 @@ struct PCfg {
   static constexpr int kOffK = kNT * kQTileBytes;
   static constexpr int kOffV = kOffK + 2 * kKVBytes;
   static constexpr int kOffInfo = kOffV + 2 * kKVBytes;
-  static constexpr int kInfoFloats = 3 * 8 + 4;   // k factor, log2 v factor, its inverse; vref
+  // k scale, log2 of the V scale, its inverse / 2^20; largest and smallest log2
+  static constexpr int kInfoFloats = 3 * 8 + 4;
   static constexpr int kOffBar = kOffInfo + kInfo * kInfoFloats * 4;
   // k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2],
   // o_done[2], info_full[4], drain, all_done[2]
@@ -205,10 +209,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// raise mx to the largest score of the first `left` tokens of a 16-token group
-// (all of them unless cut); in: the group's constants
-__device__ __forceinline__ void group_max(float *x, const float *in, float inv, bool cut,
-                                          int left, float &mx) {
+// the largest score of the first `left` tokens of a 16-token group (all of them
+// unless cut); in: the group's constants
+__device__ __forceinline__ float group_max(float *x, const float *in, float inv, bool cut,
+                                           int left) {
   if (cut) {
     // unseen tokens repeat the first one
 #pragma unroll
@@ -220,16 +224,16 @@ __device__ __forceinline__ void group_max(float *x, const float *in, float inv, 
   g0 = max3(g0, x[10], x[11]);
   g1 = max3(g1, x[12], x[13]);
   g0 = max3(g0, x[14], x[15]);
-  // unmapped groups have a log2 factor of -inf
+  // unmapped groups have a log2 scale of -inf
   const float y = fmaxf(g0, g1) * (inv * in[0]);
-  mx = fmaxf(mx, in[8] == -INFINITY || (cut && left <= 0) ? -INFINITY : y);
+  return in[8] == -INFINITY || (cut && left <= 0) ? -INFINITY : y;
 }
-// a group of scores -> p' as fp16 at `to`; l grows by its probabilities.  CUT:
-// only the first `left` tokens are seen.
+// a group of scores -> p' as fp16 at `to`; l grows by p' / v_scale / 2^20.
+// CUT: only the first `left` tokens are seen.
 template <bool CUT>
-__device__ __forceinline__ void group_exp(const float *s, const float *in, float inv, float m,
+__device__ __forceinline__ void group_exp(const float *s, const float *in, float inv, float ve,
                                           int left, float &l, uint32_t to) {
-  const float f = inv * in[0], c = in[8] - m;
+  const float f = inv * in[0], c = in[8] - ve;
   const float2 f2 = make_float2(f, f), c2 = make_float2(c, c);
   float2 p[8];
 #pragma unroll
@@ -251,7 +255,7 @@ __device__ __forceinline__ void group_exp(const float *s, const float *in, float
   for (int o = 4; o > 0; o >>= 1)
 #pragma unroll
     for (int e = 0; e < o; e++) p[e] = add2(p[e], p[e + o]);
-  l = fmaf(p[0].x + p[0].y, in[16], l);
+  if (!CUT || left > 0) l = fmaf(p[0].x + p[0].y, in[16], l);
 }
 
 // ---- work
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
     const int lim = live ? max(0, len - nq + qi + 1) : 1 << 30;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // 32 lanes a warp
     const uint32_t o_at = lanes + C::kColO + wg * D;
-    float m = -1e30f, l = 0.f, vref = 0x1p-100f;
+    float ve = -1e30f, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n_tiles; j++) {
       const int i = j * nt + wg, buf = i & 1;
@@ -544,16 +548,27 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       for (int ch = 1; ch < kBN / 32; ch++) after_wait(s[ch]);
 #pragma unroll
       for (int gr = 0; gr < C::kGroups; gr++)
-        group_max(s[gr / 2] + 16 * (gr & 1), in + gr, inv, cut, lim - tok - 16 * gr, mx);
-      const float nref = in[24];
-      const bool grow = mx > m + 8.f;
-      if (__any_sync(0xffffffffu, grow) || nref != vref) {
-        const float mn = grow ? mx : m;
-        const float al = ex2(m - mn);
-        l *= al;
-        m = mn;
-        if (j > 0) {
-          const float f = al * __fdiv_rn(vref, nref);
+        mx = fmaxf(mx, group_max(s[gr / 2] + 16 * (gr & 1), in + gr, inv, cut, lim - tok - 16 * gr));
+      // (with the tile's largest V scale in the place of each group's: a bound)
+      if (__any_sync(0xffffffffu, mx > ve + 14.f - in[24])) {
+        // the bound serves where the tile's V scales are no more than 4 apart
+        float mvx = mx + in[24];
+        if (!(in[24] - in[25] <= 2.f)) {
+          mvx = -INFINITY;
+#pragma unroll 1
+          for (int gr = 0; gr < C::kGroups; gr++) {
+            float x[16];
+            t5_ld16(s_at + 16 * gr, x);
+            t5_wait_ld(x);
+            mvx = fmaxf(mvx, in[8 + gr] + group_max(x, in + gr, inv, cut, lim - tok - 16 * gr));
+          }
+        }
+        // an integer, so that f is a power of two
+        const float vn = mvx > ve + 14.f ? ceilf(mvx) - 6.f : ve;
+        const float f = ex2(ve - vn);
+        l *= f;
+        ve = vn;
+        if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
           if (!wait(o_done + 8 * wg, (j - 1) & 1)) {
             ok = false;
             break;
@@ -573,13 +588,12 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
             }
           }
         }
-        vref = nref;
       }
       // probabilities, over the scores that were read
       if (!cut) {
 #pragma unroll
         for (int gr = 0; gr < C::kGroups; gr++)
-          group_exp<false>(s[gr / 2] + 16 * (gr & 1), in + gr, inv, m, 0, l, s_at + 8 * gr);
+          group_exp<false>(s[gr / 2] + 16 * (gr & 1), in + gr, inv, ve, 0, l, s_at + 8 * gr);
       } else {
         // the tiles at the end of a row's tokens: group_max has changed the
         // scores, so they are read again
@@ -588,7 +602,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
           float x[16];
           t5_ld16(s_at + 16 * gr, x);
           t5_wait_ld(x);
-          group_exp<true>(x, in + gr, inv, m, lim - tok - 16 * gr, l, s_at + 8 * gr);
+          group_exp<true>(x, in + gr, inv, ve, lim - tok - 16 * gr, l, s_at + 8 * gr);
         }
       }
       t5_wait_st();
@@ -602,8 +616,12 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
     t5_after();
     const bool direct = pieces == 1;
     const float nan = __int_as_float(0x7fc00000);
-    float norm = vref * 0x1p-6f;
-    if (direct) norm = l > 0.f ? norm / l : l == 0.f ? 0.f : l;
+    // a record holds l in [1, 2) and O for it
+    const float e = l > 0.f ? floorf(log2f(l)) : 0.f;
+    float norm = direct ? 0x1p-20f / l : ex2(-20.f - e);
+    if (!(l > 0.f)) norm = l;
+    float m = ve + 20.f + e;
+    if (!direct) l *= ex2(-e);
     if (!ok) norm = m = l = nan;
     const int64_t orow = (int64_t)(q0 + qi) * a.q.num_heads + head;
     float *rec = a.ws + (((int64_t)job.tail * job.pieces + job.piece) * C::kRows + wg * 128 + r) * (D + 4);
@@ -645,7 +663,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       if (!direct)
         rec[0] = m, rec[1] = l;
       else if (a.lse != nullptr)
-        a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+        a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (ve + 20.f + log2f(l));
     }
     }
   } else if (warp < kIssueWarp) {
@@ -704,7 +722,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     };
     uint4 kx[kPer], vx[kPer];
-    float vref = 0x1p-100f;
+    float most = -INFINITY;  // log2 of the largest V scale so far
     int slots = slots_of(0), next = slots_of(1);
     copy(c.k_codes, 0, slots, kx);
     copy(c.v_codes, 0, slots, vx);
@@ -723,22 +741,27 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       if (warp == C::kSoft / 32) {
         // the tile's group constants; slot j % 4 was last read for tile j - 4,
         // whose second product was waited for before V of tile j - 2 was stored
-        float vm = vs;
+        // infinite and NaN scales spoil the scores
+        const bool fine = vs - vs == 0.f;
+        float lv = fine ? log2f(vs) : 0.f;
+        float hi = slots >= 0 ? lv : -INFINITY, lo;
 #pragma unroll
-        for (int o = 1; o < C::kGroups; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-        if (vm > vref) vref = __uint_as_float((__float_as_uint(vm) + 0x7fffffu) & 0x7f800000u);
-        // blocks of scale 0 hold zeros: any factor serves.  Below 2^-40 of
-        // vref nothing reaches fp16's range: the factor stops at 2^-46, so
-        // that l keeps its terms
-        const float ratio = vs == 0.f ? 1.f : __fdiv_rn(vs, vref);
-        float lv = fmaxf(log2f(ratio), -46.f) + 6.f;
-        if (ratio != ratio) lv = ratio;
+        for (int o = 1; o < C::kGroups; o <<= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        most = fmaxf(most, hi);
+        // (an append makes no scale below 2^-107 but 0)
+        lv = fmaxf(lv, fmaxf(most - 97.f, -108.f));
+        hi = slots >= 0 ? lv : -INFINITY, lo = slots >= 0 ? lv : INFINITY;
+#pragma unroll
+        for (int o = 1; o < C::kGroups; o <<= 1) {
+          hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+          lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        }
         float *in = info + (j & 3) * C::kInfoFloats;
         if (lane < C::kGroups) {
-          in[lane] = ks;
+          in[lane] = fine ? ks : vs - vs;
           in[8 + lane] = slots >= 0 ? lv : -INFINITY;
-          in[16 + lane] = slots >= 0 ? ex2(-lv) : 0.f;
-          if (lane == 0) in[24] = vref;
+          in[16 + lane] = slots >= 0 ? ex2(-20.f - lv) : 0.f;
+          if (lane == 0) in[24] = hi, in[25] = lo;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(info_full + 8 * (j & 3));

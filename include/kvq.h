@@ -543,8 +543,11 @@ typedef struct {
  *   (NULL if that is 0); calls that may run at the same time need one each.
  * A query that attends to no token (or to unmapped blocks only) gives zeros
  * and an lse of -inf.  Queries enter the products with an error of at most
- * 2^-22 (KVQ_F32: 2^-29) of the row's largest element; probabilities meet V
- * with 11 bits (KVQ_F32: 22). */
+ * 2^-22 (KVQ_F32: 2^-29) of the row's largest element.  A token's probability
+ * times its block's V scale meets the codes with 11 bits (KVQ_F32: 22), or with
+ * an error of 2^-28 of the row's largest such product.  Weights 2^-112 below the
+ * row's largest count as 0, and V scales 2^-97 below the largest of the sequence
+ * may count as that. */
 KVQ_API size_t kvq_b8_attn_workspace(const kvq_b8_cache *cache, kvq_dtype dtype,
                                      int32_t num_q_heads, int32_t batch, int32_t max_q,
                                      int32_t max_seq_len);

@@ -392,8 +392,8 @@ def test_wide_ranges_of_values(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("nq", [1, 3])
-@pytest.mark.parametrize("span", [10, 30, 60])
+@pytest.mark.parametrize("nq,span", [(1, 10), (1, 30), (1, 60), (3, 10), (3, 30), (3, 60), (80, 10),
+                                     (80, 30), (80, 45)])
 @pytest.mark.parametrize("lean", [0.0, 0.5, 1.0, 2.0])
 @pytest.mark.parametrize("zeros", [False, True])
 def test_blocks_of_far_scales(dtype, nq, span, lean, zeros):
@@ -431,12 +431,13 @@ def test_blocks_of_far_scales(dtype, nq, span, lean, zeros):
     p = torch.exp(s - wlse[..., None])
     scale_of = r.scales["v"][r.table[0]].double()[:, 0].repeat_interleave(block)[:n]
     # P * v_scale: fp16's half step of itself, or of its subnormals, 2^-25, in
-    # units where the row's largest is 2^5 at least (see `tolerance` for the rest).
+    # units where the row's largest is 2^5 at least, or 2^3 with many rows, where a
+    # scale up to 4 times its own may set them (see `tolerance` for the rest).
     # Weights below 2^-112 of the row's largest leave fp32's range on the way.
     gone = torch.where(p < p.amax(-1, keepdim=True) * 2.0 ** -112, p, 0.0)
     tol, ltol = tolerance(dtype, dim, n, a, want * 0, torch.tensor(1.0))
     tol = (tol * (p @ v[0].abs())
-           + 2.0 ** -30 * (p * scale_of).amax(-1, keepdim=True) * 127 * n
+           + 2.0 ** (-30 if nq < 48 else -28) * (p * scale_of).amax(-1, keepdim=True) * 127 * n
            + gone @ v[0].abs() + want.abs() * (2.0 ** -8 if dtype == BF16 else 2.0 ** -24))
     err = (out.double().cpu() - want).abs()
     assert (err <= tol).all(), (err / tol).max()
@@ -444,7 +445,7 @@ def test_blocks_of_far_scales(dtype, nq, span, lean, zeros):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("nq", [1, 40])
+@pytest.mark.parametrize("nq", [1, 40, 140])
 def test_scales_as_far_as_they_go(dtype, nq):
     """Scales of 2^-107 and 2^100, weights that lean 2^-240 the other way: what
     fp32 cannot hold counts as nothing, and nothing becomes NaN."""
