@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kCombine) b8_combine_kernel(const __grid_const
   const int len = seq_len(a.q, a.c, b);
   const int i_last = (min(rt * R + R, n_rows) - 1) / a.q.group;
   const int hi_lim = max(0, len - nq + i_last + 1);
-  const int n = max(1, (hi_lim + a.p.split_tokens - 1) / a.p.split_tokens);
+  const int n = (int)max((int64_t)1, ((int64_t)hi_lim + a.p.split_tokens - 1) / a.p.split_tokens);
   const float *rec = a.ws + ((int64_t)unit * a.p.splits * R + r) * (D + 4);
   const int64_t step = (int64_t)R * (D + 4);
   float M = kEmpty;

@@ -657,6 +657,43 @@ def test_evict_long_and_equal_weights():
     assert (wide[..., :keep] == 0.25).all() and (wide[..., keep:] == 0).all()
 
 
+def far_table(first, cols, bs, n):
+    """A table of `cols` columns whose blocks are mapped from column `first` on."""
+    t = torch.full((1, cols), -1, dtype=torch.int32, device="cuda")
+    t[0, first:first + n] = torch.arange(n, dtype=torch.int32, device="cuda")
+    return t
+
+
+def near_and_far(dim, hkv, tail):
+    """The same last tokens at the end of a short table and of one of almost 2^31
+    tokens, the others unmapped: (cache, length) twice."""
+    bs, n = 256, 6
+    g = torch.Generator().manual_seed(175)
+    codes = [torch.randint(-127, 128, (n, hkv, bs, dim), generator=g, dtype=torch.int8).cuda()
+             for _ in "kv"]
+    scales = [torch.rand((n, hkv), generator=g).cuda() / 64 for _ in "kv"]
+    cols = (2 ** 31 - 4096) // bs - 1
+    far = kvq.B8Cache.wrap(codes[0], scales[0], codes[1], scales[1], far_table(cols - n, cols, bs, n))
+    near = far.with_block_table(far_table(0, n, bs, n))
+    return (near, n * bs - tail), (far, cols * bs - tail)
+
+
+@pytest.mark.parametrize("dtype,hkv,hq", [(BF16, 1, 1), (F32, 1, 16), (BF16, 4, 4)])
+def test_decode_at_the_end_of_the_longest_table(dtype, hkv, hq):
+    q = rand(176, 1, hq, 64, dtype=dtype)
+    got = [kvq.b8_attn(c, q, ints([n]), n, 0.1, return_lse=True)
+           for c, n in near_and_far(64, hkv, 37)]
+    # The same tokens in other splits.  Each side: 1499 / 16 sums at 2^-23, exp2 and
+    # scores below 16 at 2^-19, and for bf16 11 bits of P, of at most 2 (the largest
+    # value), then one rounding.
+    tol = 2 * 2 * (94 * 2.0 ** -23 + 2.0 ** -19 + (2.0 ** -11 if dtype == BF16 else 0.0))
+    if dtype == BF16:
+        tol = tol + 2 * 2.0 ** -8 * got[0][0].abs()
+    assert got[0][0].any()
+    assert ((got[0][0] - got[1][0]).abs() <= tol).all()
+    assert ((got[0][1] - got[1][1]).abs() <= 2.0 ** -15).all()
+
+
 def test_evict_nothing():
     """A batch without a token, of a longest length of 0."""
     c, _ = filled(95, [0, 0], 2, 64, 16)
