@@ -69,7 +69,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int nq = query_range(a.q, b, q0);
   const int n_rows = nq * a.q.group;
   const int len = seq_len(a.q, c, b);
-  const int t0 = range * a.range_tokens, t1 = min(len, t0 + a.range_tokens);
+  // (the last range may end past 2^31)
+  const int t0 = range * a.range_tokens, t1 = (int)min((int64_t)len, (int64_t)t0 + a.range_tokens);
   if (n_rows == 0 || t0 >= t1) return;
 
   uint32_t *qimg = reinterpret_cast<uint32_t *>(smem + C::kOffQ);

@@ -694,6 +694,21 @@ def test_decode_at_the_end_of_the_longest_table(dtype, hkv, hq):
     assert ((got[0][1] - got[1][1]).abs() <= 2.0 ** -15).all()
 
 
+@pytest.mark.parametrize("dtype,nq", [(BF16, 1), (F32, 1), (BF16, 20), (F32, 20)])
+def test_mass_at_the_end_of_the_longest_table(dtype, nq):
+    q = rand(177, nq, 2, 64, dtype=dtype)
+    kw = dict(cu_q=ints([0, nq]), max_q=nq)
+    got, lse = [], None
+    for c, n in near_and_far(64, 1, 37):
+        m = torch.zeros((1, 1, n), device="cuda")
+        if lse is None:
+            lse = kvq.b8_attn(c, q, ints([n]), n, 0.1, return_lse=True, **kw)[1]
+        kvq.b8_attn_mass(c, q, lse, ints([n]), n, 0.1, m, **kw)
+        got.append(m[0, 0, n - 1400:].clone())
+    # a token's sum has the same order in every split
+    assert got[0].all() and torch.equal(*got)
+
+
 def test_evict_nothing():
     """A batch without a token, of a longest length of 0."""
     c, _ = filled(95, [0, 0], 2, 64, 16)
