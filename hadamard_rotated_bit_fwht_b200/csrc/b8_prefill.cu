@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
   if (job.tail >= 0 && job.piece == 0 && tid == 0)
     metas(a, C::kRows, D)[job.tail] = make_int4(pieces > 1 ? b : -1, kvh, rt, job.pieces << 16 | pieces);
   const int t0 = job.piece * per * kBN;
-  const int t1 = min(hi_lim, t0 + per * kBN);
+  const int t1 = (int)min((int64_t)hi_lim, (int64_t)t0 + (int64_t)per * kBN);  // (past 2^31)
   const int nt = C::kNT == 2 && n_rows - row0 > 128 ? 2 : 1;
   const int n_tiles = t1 > t0 ? (t1 - t0 + kBN - 1) / kBN : 0;
   const int n_items = n_tiles * nt;
@@ -677,9 +677,10 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
     // lane l: block of 16-token group l % kGroups of tile j, -1 if unmapped or
     // past the range
     auto slots_of = [&](int j) {
-      const int t = t0 + j * kBN + (lane % C::kGroups) * 16;
       int p = -1;
-      if (j < n_tiles && t < t1) {
+      if (j >= n_tiles) return p;
+      const int t = t0 + j * kBN + (lane % C::kGroups) * 16;
+      if (t < t1) {
         p = __ldg(table + (t >> shift));
         if (p < 0 || p >= c.num_blocks || !in_bounds(p, p + 1, c.num_blocks, a.err)) p = -1;
       }
@@ -695,10 +696,11 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       // first code of the lane's group; groups without a block take block 0's
       // codes, which meet probabilities of 0 (a choice between a load and a zero
       // would wait for the load right here)
-      const int t = t0 + j * kBN + (lane % C::kGroups) * 16;
       int64_t off = 0;
-      if (slots >= 0)
+      if (slots >= 0) {
+        const int t = t0 + j * kBN + (lane % C::kGroups) * 16;
         off = ((((int64_t)slots * c.num_kv_heads + kvh) << shift) + (t & (bs - 1))) * D;
+      }
 #pragma unroll
       for (int i = 0; i < kTr; i++) {
         const int tr = 32 * i + r4;

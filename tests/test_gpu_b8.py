@@ -694,6 +694,17 @@ def test_decode_at_the_end_of_the_longest_table(dtype, hkv, hq):
     assert ((got[0][1] - got[1][1]).abs() <= 2.0 ** -15).all()
 
 
+def test_prompt_at_the_end_of_the_longest_table():
+    q = rand(178, 130, 1, 64, dtype=BF16)
+    got = [kvq.b8_attn(c, q, ints([n]), n, 0.1, cu_q=ints([0, 130]), max_q=130, return_lse=True)
+           for c, n in near_and_far(64, 1, 37)]
+    # the same tokens in other pieces: see the decode above, 24 tiles' sums a piece
+    tol = 4 * (94 * 2.0 ** -23 + 2.0 ** -19 + 2.0 ** -11) + 2 * 2.0 ** -8 * got[0][0].abs()
+    assert got[0][0].any()
+    assert ((got[0][0] - got[1][0]).abs() <= tol).all()
+    assert ((got[0][1] - got[1][1]).abs() <= 2.0 ** -15).all()
+
+
 @pytest.mark.parametrize("dtype,nq", [(BF16, 1), (F32, 1), (BF16, 20), (F32, 20)])
 def test_mass_at_the_end_of_the_longest_table(dtype, nq):
     q = rand(177, nq, 2, 64, dtype=dtype)
