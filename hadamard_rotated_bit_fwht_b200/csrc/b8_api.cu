@@ -14,6 +14,12 @@ kvq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// do the ranges of na and nb 4-byte values share one
+bool overlap(const void *a, __int128 na, const void *b, __int128 nb) {
+  const __int128 x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + 4 * nb && y < x + 4 * na;
+}
+
 bool good_dtype(kvq_dtype t) { return t == KVQ_F32 || t == KVQ_BF16; }
 
 kvq_status check_heads(const kvq_heads *x) {
@@ -238,10 +244,23 @@ kvq_status kvq_b8_evict(const kvq_b8_cache *src, const kvq_b8_cache *dst, int32_
       keep > (int64_t)dst->max_blocks_per_seq * dst->block_size)
     return KVQ_ERR_INVALID_ARG;
   if (batch == 0) return KVQ_OK;
-  if (!d_seq_lens || new_lens == d_seq_lens || (!mass && max_seq_len > 0) || !new_lens || !kept ||
-      !mass_out || mass_out == mass || mass_stride < max_seq_len ||
-      mass_out_stride < keep)
+  if (!d_seq_lens || (!mass && max_seq_len > 0) || !new_lens || !kept || !mass_out ||
+      mass_stride < max_seq_len || mass_out_stride < keep)
     return KVQ_ERR_INVALID_ARG;
+  // outputs are no inputs, nor each other: some CTAs have written before others read
+  const __int128 rows = (__int128)batch * src->num_kv_heads;
+  const struct {
+    const void *at;
+    __int128 n;
+  } out[3] = {{new_lens, batch}, {kept, rows * keep}, {mass_out, rows * mass_out_stride}};
+  for (int i = 0; i < 3; i++) {
+    if (overlap(out[i].at, out[i].n, d_seq_lens, batch)) return KVQ_ERR_INVALID_ARG;
+    if (max_seq_len > 0 &&
+        overlap(out[i].at, out[i].n, mass, (rows - 1) * mass_stride + max_seq_len))
+      return KVQ_ERR_INVALID_ARG;
+    for (int j = 0; j < i; j++)
+      if (overlap(out[i].at, out[i].n, out[j].at, out[j].n)) return KVQ_ERR_INVALID_ARG;
+  }
   if (2LL * batch * src->num_kv_heads >= (1LL << 31) / (keep / dst->block_size + 1))
     return KVQ_ERR_UNSUPPORTED;
   return from_cuda(launch_b8_evict(*src, *dst, batch, d_seq_lens, max_seq_len, mass, mass_stride,

@@ -579,12 +579,13 @@ KVQ_API kvq_status kvq_b8_attn_mass(const kvq_b8_cache *cache, const kvq_b8_quer
  *   or another cache.  Blocks of dst must be no blocks of src that the call
  *   reads, and dst's table must hold keep tokens a sequence.
  *   mass: device fp32 [batch][num_kv_heads][mass_stride].
- *   new_lens: device int32[batch], not d_seq_lens itself: min(n, keep);
+ *   new_lens: device int32[batch]: min(n, keep);
  *   kept: device int32[batch][num_kv_heads][keep], the kept tokens' old
  *   indices, -1 behind the last;
- *   mass_out: device fp32 [batch][num_kv_heads][mass_out_stride], not
- *   overlapping mass, mass_out_stride >= keep: the kept tokens' mass, 0 behind
- *   the last.
+ *   mass_out: device fp32 [batch][num_kv_heads][mass_out_stride],
+ *   mass_out_stride >= keep: the kept tokens' mass, 0 behind the last.
+ * new_lens, kept and mass_out overlap neither one another nor mass and
+ * d_seq_lens.
  * recent + sinks <= keep, keep >= 1. */
 KVQ_API kvq_status kvq_b8_evict(const kvq_b8_cache *src, const kvq_b8_cache *dst, int32_t batch,
                                 const int32_t *d_seq_lens, int32_t max_seq_len,

@@ -210,6 +210,46 @@ def test_evict_outputs_are_no_inputs(L, p16):
         assert evict(**kw) == INVALID, kw
 
 
+def test_each_refusal_of_evict_alone(L):
+    """Pointers and caches that are all fine, then one argument that is not."""
+    P = lambda i: (i + 1) << 20
+
+    def cache(at, **kw):
+        d = cache_desc(P(0), **kw)
+        d.k_codes, d.k_scales, d.v_codes, d.v_scales, d.block_table = (P(at + i) for i in range(5))
+        return d
+
+    base = dict(src=cache(0), dst=cache(5), batch=2, lens=P(10), max_len=64, mass=P(11), ms=64,
+                keep=8, recent=2, sinks=2, new=P(12), kept=P(13), out=P(14), mo=8)
+
+    def evict(**kw):
+        a = {**base, **kw}
+        return L.kvq_b8_evict(C.byref(a["src"]), C.byref(a["dst"]), a["batch"], a["lens"], a["max_len"],
+                              a["mass"], a["ms"], a["keep"], a["recent"], a["sinks"], a["new"],
+                              a["kept"], a["out"], a["mo"], None)
+
+    if not torch.cuda.is_available():  # all fine: as far as the launch
+        assert evict() == kvq.KVQ_ERR_CUDA
+        # side by side is fine: 2 sequences, 2 heads
+        assert evict(new=P(10) + 8, kept=P(11) + 4 * (3 * 64 + 64),
+                     out=P(13) + 4 * 4 * 8) == kvq.KVQ_ERR_CUDA
+    assert evict(batch=0) == kvq.KVQ_OK
+    for kw in (dict(batch=-1), dict(batch=3), dict(src=cache(0, seqs=1)), dict(dst=cache(5, seqs=1)),
+               dict(max_len=-1), dict(keep=0), dict(recent=-1), dict(sinks=-1),
+               dict(recent=7), dict(sinks=7), dict(recent=(1 << 31) - 1, sinks=(1 << 31) - 1),
+               dict(keep=65, mo=65), dict(dst=cache(5, hkv=1)), dict(dst=cache(5, dim=64)),
+               dict(lens=None), dict(mass=None), dict(new=None), dict(kept=None), dict(out=None),
+               dict(ms=63), dict(mo=7),
+               # outputs that are inputs or one another, whole or in part
+               dict(new=P(10)), dict(kept=P(10)), dict(out=P(10)), dict(new=P(10) + 4),
+               dict(kept=P(10) - 4 * (4 * 8 - 1)), dict(new=P(11)), dict(kept=P(11)),
+               dict(out=P(11)), dict(out=P(11) + 4 * 255), dict(out=P(11) - 4 * 31),
+               dict(new=P(13) + 4 * 31), dict(kept=P(14)), dict(out=P(12) + 4)):
+        assert evict(**kw) == INVALID, kw
+    for kw in (dict(src=cache(0, dim=96), dst=cache(5, dim=96)), dict(dst=cache(5, bs=24))):
+        assert evict(**kw) == UNSUPPORTED, kw
+
+
 def test_bindings_check_shapes_first():
     z = lambda *s, t=torch.float32: torch.zeros(s, dtype=t)
     with pytest.raises(ValueError, match="codes"):
