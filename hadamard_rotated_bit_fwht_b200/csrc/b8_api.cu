@@ -247,6 +247,11 @@ kvq_status kvq_b8_evict(const kvq_b8_cache *src, const kvq_b8_cache *dst, int32_
   if (!d_seq_lens || (!mass && max_seq_len > 0) || !new_lens || !kept || !mass_out ||
       mass_stride < max_seq_len || mass_out_stride < keep)
     return KVQ_ERR_INVALID_ARG;
+  // the same table over the same planes: every block would be read and written
+  if (src->block_table == dst->block_table &&
+      (src->k_codes == dst->k_codes || src->v_codes == dst->v_codes ||
+       src->k_scales == dst->k_scales || src->v_scales == dst->v_scales))
+    return KVQ_ERR_INVALID_ARG;
   // outputs are no inputs, nor each other: some CTAs have written before others read
   const __int128 rows = (__int128)batch * src->num_kv_heads;
   const struct {

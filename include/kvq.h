@@ -577,7 +577,8 @@ KVQ_API kvq_status kvq_b8_attn_mass(const kvq_b8_cache *cache, const kvq_b8_quer
  * were.
  *   src, dst: equal heads and dims; the same planes under another block table
  *   or another cache.  Blocks of dst must be no blocks of src that the call
- *   reads, and dst's table must hold keep tokens a sequence.
+ *   reads (the same table over the same planes is refused; two tables that share
+ *   blocks cannot be told here), and dst's table must hold keep tokens a sequence.
  *   mass: device fp32 [batch][num_kv_heads][mass_stride].
  *   new_lens: device int32[batch]: min(n, keep);
  *   kept: device int32[batch][num_kv_heads][keep], the kept tokens' old

@@ -250,6 +250,29 @@ def test_each_refusal_of_evict_alone(L):
         assert evict(**kw) == UNSUPPORTED, kw
 
 
+def test_evict_onto_its_own_blocks(L):
+    P = lambda i: (i + 1) << 20
+
+    def cache(*at):
+        d = cache_desc(P(0))
+        d.k_codes, d.k_scales, d.v_codes, d.v_scales, d.block_table = (P(i) for i in at)
+        return d
+
+    def evict(src, dst, batch=1):
+        return L.kvq_b8_evict(C.byref(src), C.byref(dst), batch, P(20), 64, P(21), 64, 8, 2, 2, P(22),
+                              P(23), P(24), 8, None)
+
+    src = cache(0, 1, 2, 3, 4)
+    assert evict(src, src, batch=0) == kvq.KVQ_OK
+    assert evict(src, src) == INVALID
+    for shared in range(4):  # any plane in common
+        at = [0 + i if i == shared else 10 + i for i in range(4)] + [4]
+        assert evict(src, cache(*at)) == INVALID, shared
+    if not torch.cuda.is_available():  # another table, or other planes: as far as the launch
+        assert evict(src, cache(0, 1, 2, 3, 9)) == kvq.KVQ_ERR_CUDA
+        assert evict(src, cache(10, 11, 12, 13, 4)) == kvq.KVQ_ERR_CUDA
+
+
 def test_bindings_check_shapes_first():
     z = lambda *s, t=torch.float32: torch.zeros(s, dtype=t)
     with pytest.raises(ValueError, match="codes"):
