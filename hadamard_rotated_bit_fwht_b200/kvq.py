@@ -702,7 +702,8 @@ def b8_evict(cache: B8Cache, into: B8Cache, mass: torch.Tensor, seq_lens: torch.
              mass_out: torch.Tensor | None = None, stream=None):
     """Keep, for each sequence and kv head, the first `sinks`, the last `recent`
     and the heaviest other tokens, `keep` in all, as tokens 0, 1, ... of
-    `into`, whose blocks must not be blocks of `cache`'s sequences.  Returns
+    `into`, whose blocks must not be blocks of `cache`'s sequences.  A kept token
+    without a block becomes a row of zeros, which attention then sees.  Returns
     (lengths [batch], kept old indices [batch, Hkv, keep], their mass [batch,
     Hkv, keep] or mass_out) (kvq_b8_evict)."""
     return bind().evict(cache._bound, into._bound, mass, seq_lens, max_seq_len, keep, recent, sinks,

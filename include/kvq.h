@@ -575,6 +575,9 @@ KVQ_API kvq_status kvq_b8_attn_mass(const kvq_b8_cache *cache, const kvq_b8_quer
  * `dst`: their stored values are quantized again as a fresh append of K and V
  * would (no rope).  Rows of a block behind the last kept token stay as they
  * were.
+ * Tokens on unmapped blocks of src count like the others, by their index and
+ * their mass.  One that is kept becomes a row of zeros on a mapped block of dst:
+ * attention left it out before and sees it afterwards, with a score of 0.
  *   src, dst: equal heads and dims; the same planes under another block table
  *   or another cache.  Blocks of dst must be no blocks of src that the call
  *   reads (the same table over the same planes is refused; two tables that share

@@ -657,6 +657,31 @@ def test_evict_long_and_equal_weights():
     assert (wide[..., :keep] == 0.25).all() and (wide[..., keep:] == 0).all()
 
 
+@pytest.mark.parametrize("keep", [64, 40])
+def test_evicted_tokens_without_a_block_become_zeros(keep):
+    """Left out by attention before, rows of zeros of score 0 afterwards, whether
+    tokens were dropped or not."""
+    c, _ = filled(94, [64], 2, 64, 16, unmapped=[(0, 1)])
+    into, _ = filled(95, [64], 2, 64, 16)
+    q = rand(96, 1, 4, 64)
+    before = kvq.b8_attn(c, q, ints([64]), 64, 0.1, return_lse=True)[1]
+    m = torch.zeros((1, 2, 64), device="cuda")
+    m[:, :, 16:32] = 1.0  # the heaviest are those without a block
+    ln, kept, _ = kvq.b8_evict(c, into, m, ints([64]), 64, keep)
+    assert ln.tolist() == [keep] and (kept[0, :, :keep] == torch.arange(keep, device="cuda")).all()
+    k, v = kvq.b8_gather(into, ints([0]), ints([keep]), keep, F32)
+    old_k, _ = kvq.b8_gather(c, ints([0]), ints([64]), 64, F32)
+    assert not k[:, 16:32].any() and not v[:, 16:32].any() and k[:, :16].any()
+    _, after, _, _, _, _ = check_attention(into, q, [keep], None, keep, F32, 0.1)
+    if keep == 64:
+        # 16 terms of exp(0) more.  Every block holds a code of 127 or -127, so its
+        # codes stay and its scale is rounded twice, 2^-24 each: scores below 32 and
+        # their sums are off by 2^-17 at most.
+        assert torch.allclose(k[:, 32:], old_k[:, 32:], rtol=2 ** -22)
+        want = torch.log(torch.exp(before.double()) + 16)
+        assert ((after.double() - want).abs() < 2 ** -16).all()
+
+
 def far_table(first, cols, bs, n):
     """A table of `cols` columns whose blocks are mapped from column `first` on."""
     t = torch.full((1, cols), -1, dtype=torch.int32, device="cuda")
