@@ -572,9 +572,39 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, rope:
          k_out: torch.Tensor | None = None, stream=None):
     """Rotate q and k ([..., heads, dim], any token and head stride) by their
     tokens' positions (int32); returns (q_out, k_out).  q_out and k_out may be
-    q and k themselves.  inverse turns the other way (kvq_rope)."""
+    q and k themselves.  inverse turns the other way (kvq_rope).  Gradients of q
+    and k are recorded where they are asked for, by the rotation the other way;
+    not through a q_out or k_out, and not for positions and frequencies."""
+    if (torch.is_grad_enabled() and q_out is None and k_out is None
+            and (getattr(q, "requires_grad", False) or getattr(k, "requires_grad", False))):
+        return _RopeWithGrad.apply(q, k, positions, rope, inverse, stream)
     return bind().rope(q, k, positions, rope.inv_freq, rope.interleaved, rope.factor, inverse,
                        q_out, k_out, stream)
+
+
+class _RopeWithGrad(torch.autograd.Function):
+    """The rotation is linear, and the rotation the other way (with the factor
+    kept) is its transpose."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, spec, inverse, stream):
+        ctx.save_for_backward(positions)
+        ctx.spec, ctx.inverse = spec, inverse
+        ctx.set_materialize_grads(False)
+        return bind().rope(q, k, positions, spec.inv_freq, spec.interleaved, spec.factor, inverse,
+                           None, None, stream)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        # one call for both where both are there; gradients may come expanded
+        at = [i for i, g in enumerate(grads) if g is not None and ctx.needs_input_grad[i]]
+        out = [None, None]
+        if at:
+            x = [grads[i].contiguous() for i in at] + [None]
+            got = rope(x[0], x[1], ctx.saved_tensors[0], ctx.spec, inverse=not ctx.inverse)
+            for i, g in zip(at, got):
+                out[i] = g
+        return out[0], out[1], None, None, None, None
 
 
 # --------------------------------------------------------------------------
@@ -682,7 +712,8 @@ def b8_attn(cache: B8Cache, q: torch.Tensor, seq_lens: torch.Tensor, max_seq_len
     """Attention of q [queries, Hq, dim] (any token and head stride) over the
     cache: out [queries, Hq, dim] in q's dtype, and lse [queries, Hq] fp32 if
     asked for.  One query per sequence, or sequence b's are rows cu_q[b] ..
-    cu_q[b + 1] - 1, at most max_q, under the causal rule (kvq_b8_attn)."""
+    cu_q[b + 1] - 1, at most max_q, under the causal rule (kvq_b8_attn).  No
+    gradient is recorded."""
     return bind().attn(cache._bound, q, seq_lens, max_seq_len, scale, cu_q, max_q, return_lse, out,
                        lse, workspace, stream)
 

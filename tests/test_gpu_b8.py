@@ -121,6 +121,74 @@ def test_rope_inverse_is_the_gradient():
         assert abs((f(up) - f(dn)) / 2 - grad[i, j, e].item()) < 4 * 60 * 2 ** -21
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rope_records_gradients(dtype, inverse):
+    r = kvq.Rope.make(32, interleaved=inverse, scaling="yarn", scale=4.0, trained_len=2048)
+    x, w = rand(181, 7, 6, 64, dtype=dtype), rand(182, 7, 6, 64, dtype=dtype)
+    pos = ints([0, 1, 17, 999, 32768, 100000, -3])
+    plain = kvq.rope(x[:, :4], x[:, 4:], pos, r, inverse=inverse)
+    gq, gk = kvq.rope(w[:, :4], w[:, 4:], pos, r, inverse=not inverse)
+    leaf = x.clone().requires_grad_()
+    # slices of one projection
+    q, k = kvq.rope(leaf[:, :4], leaf[:, 4:], pos, r, inverse=inverse)
+    assert torch.equal(q, plain[0]) and torch.equal(k, plain[1])
+    torch.autograd.backward((q, k), (w[:, :4], w[:, 4:]))
+    assert torch.equal(leaf.grad, torch.cat((gq, gk), 1))
+    # one of the two alone, as input or as what is used of the outputs
+    q1 = x[:, :4].clone().requires_grad_()
+    kvq.rope(q1, None, pos, r, inverse=inverse)[0].backward(w[:, :4])
+    assert torch.equal(q1.grad, gq)
+    k1 = x[:, 4:].clone().requires_grad_()
+    kvq.rope(x[:, :4], k1, pos, r, inverse=inverse)[1].backward(w[:, 4:])
+    assert torch.equal(k1.grad, gk)
+    both = [x[:, :4].clone().requires_grad_(), x[:, 4:].clone().requires_grad_()]
+    kvq.rope(*both, pos, r, inverse=inverse)[1].backward(w[:, 4:])
+    assert both[0].grad is None and torch.equal(both[1].grad, gk)
+    # a gradient that comes expanded, in batches, on another stream; a second one
+    y = x.view(1, 7, 6, 64).clone().requires_grad_()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        kvq.rope(y, None, pos, r, inverse=inverse)[0].sum().backward()
+    torch.cuda.current_stream().wait_stream(st)
+    ones = torch.ones_like(x)
+    assert torch.equal(y.grad[0], kvq.rope(ones, None, pos, r, inverse=not inverse)[0])
+    v = w.clone().requires_grad_()
+    z = x.clone().requires_grad_()
+    g, = torch.autograd.grad(kvq.rope(z, None, pos, r, inverse=inverse)[0], z, v, create_graph=True)
+    g.backward(x)
+    assert torch.equal(v.grad, kvq.rope(x, None, pos, r, inverse=inverse)[0])
+    # nothing is recorded where nothing is asked for, nor through given outputs
+    with torch.no_grad():
+        assert kvq.rope(leaf, None, pos, r)[0].grad_fn is None
+    assert kvq.rope(x, None, pos, r)[0].grad_fn is None
+    o = torch.empty_like(x)
+    assert kvq.rope(leaf, None, pos, r, q_out=o)[0] is o and o.grad_fn is None
+
+
+def test_rope_gradient_in_a_captured_step():
+    """Forward and backward captured, all of the leaf's uses on the capture's stream
+    (torch refuses a capture beside an eager graph of the same leaf on another)."""
+    r = kvq.Rope.make(64)
+    w, pos = rand(184, 5, 2, 64), ints([0, 5, 9, 100, 7])
+    want, _ = kvq.rope(w, None, pos, r, inverse=True)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        x = rand(183, 5, 2, 64).requires_grad_()
+        for _ in range(2):
+            torch.autograd.grad(kvq.rope(x, None, pos, r)[0], x, w)
+        st.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=st):
+            got, = torch.autograd.grad(kvq.rope(x, None, pos, r)[0], x, w)
+        got.zero_()
+        gr.replay()
+    st.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_rope_shapes_streams_and_empty():
     r = kvq.Rope.make(64)
     x = rand(3, 2, 5, 4, 64, dtype=BF16)
