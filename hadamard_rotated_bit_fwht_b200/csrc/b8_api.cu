@@ -1,6 +1,7 @@
 // b8_api.cu -- the extern "C" entry points of the rotary positions and of the
 // block-scaled 8-bit cache: host-side argument validation and dispatch.
 #include <math.h>
+#include <stdlib.h>
 
 #include "b8_internal.cuh"
 
@@ -133,6 +134,12 @@ kvq_status kvq_rope(const kvq_rope_spec *spec, kvq_dtype dtype, int32_t head_dim
   for (int i = 0; i < (k ? 4 : 2); i += 2) {
     const kvq_heads *a = views[i], *b = views[i + 1];
     if (a->num_heads != b->num_heads) return KVQ_ERR_INVALID_ARG;
+    // heads of an output that share elements (of a broadcast view) would be rotated
+    // more than once, or race
+    const int64_t ts = llabs(b->token_stride), hs = llabs(b->head_stride);
+    if ((num_tokens > 1 && ts < head_dim) || (b->num_heads > 1 && hs < head_dim) ||
+        (num_tokens > 1 && b->num_heads > 1 && ts == hs))
+      return KVQ_ERR_INVALID_ARG;
     // in place means the very same view
     if (a->data == b->data &&
         (a->token_stride != b->token_stride || a->head_stride != b->head_stride))

@@ -445,7 +445,8 @@ typedef struct {
  *   inverse: nonzero turns by -t: undoes the rotation (factor 1), and is its
  *   transpose, so it maps the gradient of the outputs to that of the inputs.
  *   q_out, k_out: as many heads as q and k; the same view as the input
- *   (in place) or memory that does not overlap it.
+ *   (in place) or memory that does not overlap it; no two of their heads share
+ *   an element.
  * head_dim is a multiple of 16, at most 512 (KVQ_ERR_UNSUPPORTED otherwise,
  * and for a rot_dim that is not a multiple of 16). */
 KVQ_API kvq_status kvq_rope(const kvq_rope_spec *spec, kvq_dtype dtype, int32_t head_dim,

@@ -104,6 +104,30 @@ def test_rope_refusals(L, p16):
     assert call(qo=heads(p16, token=512)) == INVALID  # in place with other strides
 
 
+def test_rope_refuses_outputs_that_share_elements(L, p16):
+    spec = kvq.RopeDesc(p16, 64, 0, 1.0)
+    x = heads(p16 + 4096)
+
+    def call(out, n=4, src=x):
+        return L.kvq_rope(C.byref(spec), 1, 128, n, p16, 0, C.byref(src), C.byref(out), None, None,
+                          None)
+
+    for token, head in ((0, 128), (256, 0), (256, 64), (120, 512), (256, 256), (-64, 512), (512, -64)):
+        o = heads(p16, token=token, head=head)
+        assert call(o) == INVALID, (token, head)
+        assert call(o, src=o) == INVALID, (token, head)  # in place
+    if not torch.cuda.is_available():  # fine, as far as the launch
+        for o in (heads(p16, token=256, head=128), heads(p16, token=128, head=512),
+                  heads(p16, token=-256, head=128)):
+            assert call(o) == kvq.KVQ_ERR_CUDA
+        # one token, one head: their strides mean nothing
+        assert call(heads(p16, token=0, head=128), n=1) == kvq.KVQ_ERR_CUDA
+        one = heads(p16 + 4096, n=1)
+        assert call(heads(p16, n=1, token=256, head=0), src=one) == kvq.KVQ_ERR_CUDA
+        # inputs may be broadcast
+        assert call(heads(p16), src=heads(p16 + 4096, token=0, head=0)) == kvq.KVQ_ERR_CUDA
+
+
 def test_cache_refusals(L, p16):
     x = heads(p16)
 
