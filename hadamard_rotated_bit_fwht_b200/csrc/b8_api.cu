@@ -218,6 +218,8 @@ kvq_status kvq_b8_attn(const kvq_b8_cache *cache, const kvq_b8_queries *queries,
   const size_t need = b8_attn_workspace_bytes(*cache, q.batch, p);
   if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
     return KVQ_ERR_WORKSPACE;
+  // other CTAs may still read the queries when one writes its rows
+  if (out == q.q) return KVQ_ERR_INVALID_ARG;
   return from_cuda(launch_b8_attn(*cache, q, p, out, lse, static_cast<float *>(workspace),
                                   as_stream(stream)));
 }

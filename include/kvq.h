@@ -538,8 +538,8 @@ typedef struct {
 /* kvq_b8_attn -- attention over the cache: out = softmax(scale q K^T) V for
  * each query and head (head j reads kv head j / (num_q_heads / num_kv_heads)).
  *   out: device, [total_q][num_q_heads][head_dim] of q's dtype, 16-byte
- *   aligned, not overlapping q; lse: NULL or device fp32 [total_q][num_q_heads],
- *   the natural logarithm of the sum of exp(score).
+ *   aligned, not overlapping q (q itself is refused); lse: NULL or device fp32
+ *   [total_q][num_q_heads], the natural logarithm of the sum of exp(score).
  *   workspace: device, 16-byte aligned, at least kvq_b8_attn_workspace bytes
  *   (NULL if that is 0); calls that may run at the same time need one each.
  * A query that attends to no token (or to unmapped blocks only) gives zeros

@@ -195,6 +195,17 @@ def test_attention_refusals(L, p16):
     assert call(wide) == UNSUPPORTED
 
 
+def test_attention_refuses_to_write_over_its_queries(L, p16):
+    d, q = cache_desc(p16), queries(p16 + 4096)
+
+    def call(out):
+        return L.kvq_b8_attn(C.byref(d), C.byref(q), out, None, None, 0, None)
+
+    assert call(p16 + 4096) == INVALID
+    if not torch.cuda.is_available():  # elsewhere: as far as the launch
+        assert call(p16) == kvq.KVQ_ERR_CUDA
+
+
 def test_mass_and_evict_refusals(L, p16):
     d = cache_desc(p16)
 
