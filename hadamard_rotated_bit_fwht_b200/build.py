@@ -74,12 +74,22 @@ def build_bind(force: bool = False) -> str:
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Compile every .cu to an object in parallel (relocatable device code is
     not needed: no kernel calls across files), then link libkvq.so (or, with
-    debug=True, libkvq_debug.so with the bounds checks compiled in); and the
-    marshalling module of the binding."""
-    build_bind(force and not debug)
+    debug=True, libkvq_debug.so with the bounds checks compiled in).  Then, where
+    there is a torch to build it against, the marshalling module of the Python
+    binding: the library itself needs nvcc alone."""
     lib = LIB_DEBUG if debug else LIB
-    if not force and not _stale(lib):
-        return lib
+    if force or _stale(lib):
+        _build_lib(lib, verbose, debug)
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        print("no torch: the module of the Python binding is not built", file=sys.stderr)
+    else:
+        build_bind(force and not debug)
+    return lib
+
+
+def _build_lib(lib: str, verbose: bool, debug: bool) -> None:
     from concurrent.futures import ThreadPoolExecutor
     os.makedirs(OBJ_DIR, exist_ok=True)
     compile_flags = [f for f in FLAGS if f not in ("--shared",)]
@@ -105,7 +115,6 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     os.replace(tmp, lib)
     for o in objs:
         os.remove(o)
-    return lib
 
 
 if __name__ == "__main__":

@@ -1,0 +1,39 @@
+"""How the library and the binding's module are built (no GPU; the compilers are
+stand-ins that write down how they were called)."""
+import os
+import stat
+import subprocess
+import sys
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def stand_in(path, log):
+    """A compiler that makes its -o file and logs its arguments."""
+    path.write_text(f"""#!{sys.executable}
+import sys
+open({str(log)!r}, "a").write(" ".join(sys.argv) + "\\n")
+open(sys.argv[sys.argv.index("-o") + 1], "w").close()
+""")
+    path.chmod(path.stat().st_mode | stat.S_IXUSR)
+
+
+def run(code, tmp_path, **env):
+    head = ("from hadamard_rotated_bit_fwht_b200 import build\n"
+            f"build.LIB = {str(tmp_path / 'libkvq.so')!r}\n"
+            f"build.BIND = {str(tmp_path / 'kvq_bind.so')!r}\n"
+            f"build.OBJ_DIR = {str(tmp_path / 'obj')!r}\n")
+    return subprocess.run([sys.executable, "-c", code.replace("HEAD\n", head)], cwd=ROOT,
+                          env={**os.environ, **env}, capture_output=True, text=True, timeout=300)
+
+
+def test_the_library_needs_no_torch(tmp_path):
+    stand_in(tmp_path / "nvcc", tmp_path / "log")
+    r = run("import sys\nsys.modules['torch'] = None\nHEAD\nprint(build.build(force=True))", tmp_path,
+            NVCC=str(tmp_path / "nvcc"))
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.strip() == str(tmp_path / "libkvq.so")
+    assert (tmp_path / "libkvq.so").exists() and not (tmp_path / "kvq_bind.so").exists()
+    assert "binding is not built" in r.stderr
+    calls = (tmp_path / "log").read_text().splitlines()
+    assert sum(" -c " in c for c in calls) == len(calls) - 1 > 1
