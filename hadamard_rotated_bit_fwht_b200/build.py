@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
 
@@ -46,6 +47,16 @@ def _stale(lib: str = LIB) -> bool:
 OBJ_DIR = os.path.join(ROOT, "_build", "kvq")
 
 
+def _cuda_include() -> str:
+    """The headers beside nvcc, which may be a name on the PATH or a link."""
+    nvcc = shutil.which(NVCC) or NVCC
+    for p in (nvcc, os.path.realpath(nvcc)):
+        inc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(p))), "include")
+        if os.path.exists(os.path.join(inc, "cuda_runtime_api.h")):
+            return inc
+    raise FileNotFoundError(f"no cuda_runtime_api.h in the include folder of {nvcc}")
+
+
 def build_bind(force: bool = False) -> str:
     """Compile the marshalling module kvq_bind.so against the running Python and
     torch (host code only)."""
@@ -60,7 +71,7 @@ def build_bind(force: bool = False) -> str:
     t = os.path.dirname(torch.__file__)
     inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(t, "include"),
            os.path.join(t, "include", "torch", "csrc", "api", "include"),
-           os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+           _cuda_include()]
     tmp = BIND + f".tmp{os.getpid()}"
     subprocess.check_call([
         "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",

@@ -37,3 +37,24 @@ def test_the_library_needs_no_torch(tmp_path):
     assert "binding is not built" in r.stderr
     calls = (tmp_path / "log").read_text().splitlines()
     assert sum(" -c " in c for c in calls) == len(calls) - 1 > 1
+
+
+def test_nvcc_by_name(tmp_path):
+    """A name on the PATH, a link, and a path: the headers beside the compiler."""
+    cuda = tmp_path / "cuda"
+    for d in ("bin", "include"):
+        (cuda / d).mkdir(parents=True)
+    stand_in(cuda / "bin" / "nvcc", tmp_path / "log")
+    (cuda / "include" / "cuda_runtime_api.h").write_text("")
+    (tmp_path / "links").mkdir()
+    (tmp_path / "links" / "nvcc").symlink_to(cuda / "bin" / "nvcc")
+    stand_in(tmp_path / "links" / "g++", tmp_path / "gxx")
+    for nvcc, path in (("nvcc", cuda / "bin"), ("nvcc", tmp_path / "links"),
+                       (str(cuda / "bin" / "nvcc"), tmp_path), (str(tmp_path / "links" / "nvcc"), tmp_path)):
+        r = run("HEAD\nbuild.build_bind(force=True)", tmp_path, NVCC=nvcc,
+                PATH=f"{path}:{tmp_path / 'links'}:{os.environ['PATH']}")
+        assert r.returncode == 0, r.stderr
+    for call in (tmp_path / "gxx").read_text().splitlines():
+        assert f"-I{cuda / 'include'}" in call.split()
+    r = run("HEAD\nbuild.build_bind(force=True)", tmp_path, NVCC=str(tmp_path / "none" / "nvcc"))
+    assert r.returncode and "cuda_runtime_api.h" in r.stderr
