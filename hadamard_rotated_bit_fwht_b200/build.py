@@ -57,6 +57,23 @@ def _cuda_include() -> str:
     raise FileNotFoundError(f"no cuda_runtime_api.h in the include folder of {nvcc}")
 
 
+def bind_key() -> str:
+    """The Python and torch that a marshalling module belongs to."""
+    import sysconfig
+
+    import torch
+    return (f"kvq_bind for {sysconfig.get_config_var('SOABI')}, torch {torch.__version__} "
+            f"abi {int(torch.compiled_with_cxx11_abi())}")
+
+
+def bind_is_for(key: str) -> bool:
+    """Whether kvq_bind.so is there and was built for `key`, which it holds."""
+    if not os.path.exists(BIND):
+        return False
+    with open(BIND, "rb") as f:
+        return key.encode() + b"\0" in f.read()
+
+
 def build_bind(force: bool = False) -> str:
     """Compile the marshalling module kvq_bind.so against the running Python and
     torch (host code only)."""
@@ -64,7 +81,7 @@ def build_bind(force: bool = False) -> str:
 
     import torch
     src = os.path.join(CSRC, "kvq_bind.cpp")
-    if not force and os.path.exists(BIND) and all(
+    if not force and bind_is_for(bind_key()) and all(
             os.path.getmtime(p) <= os.path.getmtime(BIND)
             for p in (src, os.path.join(INCLUDE, "kvq.h"))):
         return BIND
@@ -75,6 +92,7 @@ def build_bind(force: bool = False) -> str:
     tmp = BIND + f".tmp{os.getpid()}"
     subprocess.check_call([
         "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
+        f'-DKVQ_BIND_KEY="{bind_key()}"',
         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
         *(f"-I{p}" for p in inc), src, "-o", tmp, "-L" + os.path.join(t, "lib"),
         "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"])

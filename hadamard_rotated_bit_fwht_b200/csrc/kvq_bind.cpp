@@ -461,4 +461,10 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "kvq_bind", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_kvq_bind() { return PyModule_Create(&module); }
+// KVQ_BIND_KEY: the Python and torch that this module is built for; the loader
+// looks for it in the file before it loads the module
+PyMODINIT_FUNC PyInit_kvq_bind() {
+  PyObject *m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "key", KVQ_BIND_KEY) < 0) Py_CLEAR(m);
+  return m;
+}

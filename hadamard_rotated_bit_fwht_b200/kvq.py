@@ -17,6 +17,8 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
+from . import build as _build
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # KVQ_LIBRARY may name another build of the same library (the bounds-checking
 # libkvq_debug.so); the default is the release build next to this file
@@ -172,10 +174,10 @@ def bind():
     step, which in Python would cost more than the kernels."""
     global _bind
     if _bind is None:
-        path = os.path.join(_PKG, "kvq_bind.so")
-        if not os.path.exists(path):
-            raise ImportError(f"{path} is missing: build it with "
-                              "`python -m hadamard_rotated_bit_fwht_b200.build`")
+        path = _build.BIND
+        if not _build.bind_is_for(_build.bind_key()):
+            raise ImportError(f"{path} is missing or built for another Python or torch: build it "
+                              "with `python -m hadamard_rotated_bit_fwht_b200.build`")
         spec = importlib.util.spec_from_file_location("kvq_bind", path)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)

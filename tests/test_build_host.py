@@ -58,3 +58,26 @@ def test_nvcc_by_name(tmp_path):
         assert f"-I{cuda / 'include'}" in call.split()
     r = run("HEAD\nbuild.build_bind(force=True)", tmp_path, NVCC=str(tmp_path / "none" / "nvcc"))
     assert r.returncode and "cuda_runtime_api.h" in r.stderr
+
+
+def test_a_module_of_another_torch_is_stale(tmp_path):
+    from hadamard_rotated_bit_fwht_b200 import build
+    build.build_bind()
+    key = build.bind_key()
+    assert build.bind_is_for(key)
+    assert not build.bind_is_for(key[:-1]) and not build.bind_is_for(key + "x")
+    # not loaded, and built again
+    code = ("HEAD\nbuild.BIND = {bind!r}\nbuild.bind_key = lambda: 'kvq_bind for another torch'\n"
+            "from hadamard_rotated_bit_fwht_b200 import kvq\n"
+            "try:\n    kvq.bind()\nexcept ImportError as e:\n    print('refused', e)\n"
+            "build.BIND = {copy!r}\nbuild.build_bind()\n")
+    copy = tmp_path / "copy.so"
+    copy.write_bytes(open(build.BIND, "rb").read())
+    os.utime(copy)  # newer than its sources
+    stand_in(tmp_path / "g++", tmp_path / "gxx")
+    r = run(code.format(bind=build.BIND, copy=str(copy)), tmp_path,
+            PATH=f"{tmp_path}:{os.environ['PATH']}")
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.startswith("refused") and "another Python or torch" in r.stdout
+    call, = (tmp_path / "gxx").read_text().splitlines()
+    assert '-DKVQ_BIND_KEY="kvq_bind for another torch"' in call
