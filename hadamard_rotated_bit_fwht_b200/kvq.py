@@ -556,7 +556,9 @@ class Rope:
     def make(cls, rot_dim, base=10000.0, *, interleaved=False, scaling="none", scale=1.0,
              trained_len=0, beta_fast=32.0, beta_slow=1.0, device="cuda"):
         """The frequencies of kvq_rope_frequencies; scaling: "none", "linear",
-        "ntk" or "yarn"."""
+        "ntk" or "yarn", whose ramp is linear in the number of turns.  A model
+        made with a ramp in the pair's index has other frequencies there: give
+        its own table, Rope(inv_freq, interleaved, factor)."""
         if scaling not in ROPE_SCALINGS:
             raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
         f = np.zeros(max(int(rot_dim) // 2, 1))

@@ -414,7 +414,11 @@ typedef struct {
  *   KVQ_ROPE_YARN    f_i where pair i makes at least beta_fast turns within
  *                    trained_len positions, f_i / scale where it makes at most
  *                    beta_slow, a linear ramp in the number of turns between;
- *                    the factor is 0.1 ln(scale) + 1. */
+ *                    the factor is 0.1 ln(scale) + 1.  (So the method's paper.
+ *                    Widely used code ramps linearly in the pair's index, between
+ *                    the indices of those turns rounded outwards: models made with
+ *                    that have other frequencies within the ramp, and their own
+ *                    table goes into kvq_rope_spec as it is.) */
 typedef enum {
   KVQ_ROPE_NONE = 0,
   KVQ_ROPE_LINEAR = 1,

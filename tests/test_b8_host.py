@@ -65,6 +65,26 @@ def test_frequencies(L, rot):
     assert math.isclose(m, 0.1 * math.log(s) + 1, rel_tol=1e-6)
 
 
+def test_yarn_ramps_differ_between_their_ends_only():
+    """The ramp in turns, which is offered, and the one in the pair's index: equal
+    outside, different inside, as the header says."""
+    rot, base, s, trained = 128, 10000.0, 8.0, 4096.0
+    got = kvq.Rope.make(rot, base, scaling="yarn", scale=s, trained_len=trained, device="cpu")
+    i = np.arange(rot // 2)
+    plain = base ** (-2.0 * i / rot)
+    index = lambda turns: rot * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(base))
+    low, high = math.floor(index(32.0)), math.ceil(index(1.0))
+    ramp = np.clip((i - low) / (high - low), 0, 1)
+    by_index = plain * (1 - ramp) + plain / s * ramp
+    f = got.inv_freq.numpy()
+    out = (i <= low) | (i >= high)
+    np.testing.assert_allclose(f[out], by_index[out], rtol=1e-13)
+    assert (np.abs(f / by_index - 1)[low + 2:high - 1] > 1e-2).all()
+    # such a model's own table
+    own = kvq.Rope(torch.from_numpy(by_index), False, got.factor)
+    assert own.inv_freq.dtype == torch.float64 and own.inv_freq.numel() == rot // 2
+
+
 def test_frequency_refusals():
     for kw in (dict(rot_dim=7), dict(rot_dim=0), dict(rot_dim=16, base=-1.0),
                dict(rot_dim=16, scaling="linear", scale=0.5),
