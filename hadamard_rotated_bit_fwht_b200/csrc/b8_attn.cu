@@ -367,16 +367,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
   for (int r = warp; r < R; r += kWarps) {
     const int row = row0 + r;
     if (row >= n_rows) break;
-    float M = kEmpty, L = 0.f;
+    float M = kEmpty, MV = kEmpty, L = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; w++) M = fmaxf(M, mm[w * R + r]);
+    for (int w = 0; w < kWarps; w++) M = fmaxf(M, mm[w * R + r]), MV = fmaxf(MV, mvs[w * R + r]);
     float f[kWarps];
 #pragma unroll
     for (int w = 0; w < kWarps; w++) {
       L += ex2(mm[w * R + r] - M) * ml[w * R + r];
-      f[w] = ex2(mvs[w * R + r] - M - 6.f);
+      f[w] = ex2(mvs[w * R + r] - MV);
     }
     const bool direct = a.p.splits == 1;
+    // (from units of 2^MV / 64: after the sum, which would lose terms of scales near
+    // fp32's lower end)
+    const float unit = ex2(MV - M - 6.f);
     const float norm = direct ? (L > 0.f ? __fdiv_rn(1.f, L) : L == 0.f ? 0.f : L) : 1.f;
     const int i = row / a.q.group, head = kvh * a.q.group + row - i * a.q.group;
     const int64_t orow = (int64_t)(q0 + i) * a.q.num_heads + head;
@@ -390,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
                                                            (w * R + r) * C::kRow + d);
         acc.x += f[w] * x.x, acc.y += f[w] * x.y, acc.z += f[w] * x.z, acc.w += f[w] * x.w;
       }
+      acc.x *= unit, acc.y *= unit, acc.z *= unit, acc.w *= unit;
       acc.x *= norm, acc.y *= norm, acc.z *= norm, acc.w *= norm;
       if (direct)
         store_out<D, HILO>(a.out, orow * D + d, acc);

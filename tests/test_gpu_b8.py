@@ -535,6 +535,29 @@ def test_scales_as_far_as_they_go(dtype, nq):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("nq", [1, 45])
+def test_scales_near_the_ends_of_fp32(dtype, nq):
+    """One scale for all blocks, up to what the header allows: exact; past that, no
+    finite number that is wrong."""
+    n = 300
+    c, _ = filled(179, [n], 1, 64, 16)
+    q = rand(180, nq, 2, 64, dtype=dtype)
+    for e in (-107, -60, 0, 60, 100, 104):
+        c.v_scales.fill_(2.0 ** e)
+        out, *_ = check_attention(c, q, [n], [0, nq], n, dtype, 0.05)
+        assert out.any()
+    c.v_scales.fill_(2.0 ** 110)
+    out, lse = kvq.b8_attn(c, q, ints([n]), n, 0.05, cu_q=ints([0, nq]), max_q=nq, return_lse=True)
+    r = ref.Cache(c)
+    want, wlse, _ = ref.attention(r, q, [n], [0, nq], 0.05)
+    good = torch.isfinite(out).cpu()
+    assert ((out.double().cpu() - want).abs()[good] <= 2.0 ** 117 * 2.0 ** -7).all()
+    good = torch.isfinite(lse).cpu()
+    assert ((lse.double().cpu() - wlse).abs()[good] < 1e-4).all()
+    assert not (lse == -math.inf).any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("scale", [0.0, -0.125])
 def test_other_scales(dtype, scale):
     c, _ = filled(73, [300, 40], 1, 64, 32)
