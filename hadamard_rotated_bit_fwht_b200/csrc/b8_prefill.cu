@@ -743,8 +743,9 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
       if (warp == C::kSoft / 32) {
         // the tile's group constants; slot j % 4 was last read for tile j - 4,
         // whose second product was waited for before V of tile j - 2 was stored
-        // infinite and NaN scales spoil the scores
-        const bool fine = vs - vs == 0.f;
+        // infinite and NaN scales spoil the scores, and so do those whose share of l
+        // would vanish (their sums leave fp32's range before long)
+        const bool fine = vs < 0x1p105f;
         float lv = fine ? log2f(vs) : 0.f;
         float hi = slots >= 0 ? lv : -INFINITY, lo;
 #pragma unroll
@@ -760,7 +761,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
         }
         float *in = info + (j & 3) * C::kInfoFloats;
         if (lane < C::kGroups) {
-          in[lane] = fine ? ks : vs - vs;
+          in[lane] = fine ? ks : __int_as_float(0x7fc00000);
           in[8 + lane] = slots >= 0 ? lv : -INFINITY;
           in[16 + lane] = slots >= 0 ? ex2(-20.f - lv) : 0.f;
           if (lane == 0) in[24] = hi, in[25] = lo;

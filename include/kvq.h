@@ -552,7 +552,8 @@ typedef struct {
  * times its block's V scale meets the codes with 11 bits (KVQ_F32: 22), or with
  * an error of 2^-28 of the row's largest such product.  Weights 2^-112 below the
  * row's largest count as 0, and V scales 2^-97 below the largest of the sequence
- * may count as that. */
+ * may count as that.  Sums are not scaled down: V scales have to be below 2^105,
+ * and values times the number of tokens below 2^127. */
 KVQ_API size_t kvq_b8_attn_workspace(const kvq_b8_cache *cache, kvq_dtype dtype,
                                      int32_t num_q_heads, int32_t batch, int32_t max_q,
                                      int32_t max_seq_len);

@@ -535,7 +535,7 @@ def test_scales_as_far_as_they_go(dtype, nq):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("nq", [1, 45])
+@pytest.mark.parametrize("nq", [1, 45, 140])
 def test_scales_near_the_ends_of_fp32(dtype, nq):
     """One scale for all blocks, up to what the header allows: exact; past that, no
     finite number that is wrong."""
