@@ -30,8 +30,10 @@ __device__ __forceinline__ int64_t block_of(const kvq_b8_cache &c, int b, int co
 }
 
 // amax below 2^-100 counts as 0: 1 / scale stays finite, and such values
-// vanish beside any other
+// vanish beside any other.  An infinity or a NaN makes it NaN, and with it every
+// value of the block.
 __device__ __forceinline__ float scale_of(float amax) {
+  if (amax - amax != 0.f) return __int_as_float(0x7fc00000);
   return amax < 0x1p-100f ? 0.f : __fdiv_rn(amax, 127.f);
 }
 __device__ __forceinline__ float inverse(float scale) {
@@ -41,8 +43,8 @@ __device__ __forceinline__ float inverse(float scale) {
 // rint(x) of 4 values as packed bytes.  The sum with 1.5 * 2^23 rounds to the
 // nearest even integer and leaves it in the low byte.  No clamp is needed:
 // scale >= RN(amax / 127) and |x| <= amax give |x * RN(1 / scale)| <= 127 (1 +
-// 2^-22), which rounds to 127, and old codes shrink.  NaN products (an infinite
-// input times 0) come out as some code.
+// 2^-22), which rounds to 127, and old codes shrink.  Blocks of a NaN scale get
+// codes without a meaning.
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
   constexpr float kMagic = 12582912.f;
   auto one = [](float x) { return __float_as_uint(__fadd_rn(x, kMagic)); };

@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   float amax = 0.f;
   auto raise = [&](const float (&x)[8], const float (&y)[8]) {
 #pragma unroll
-    for (int e = 0; e < 8; e++) amax = fmaxf(amax, fmaxf(fabsf(x[e]), fabsf(y[e])));
+    for (int e = 0; e < 8; e++) amax = fmax_nan(amax, fmax_nan(fabsf(x[e]), fabsf(y[e])));
   };
   if (KEEP) {
     b8::cp_wait<0>();
@@ -159,12 +159,12 @@ __global__ void __launch_bounds__(kThreads, 3)
     each([&](int, const float (&x)[8], const float (&y)[8]) { raise(x, y); });
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  for (int o = 16; o > 0; o >>= 1) amax = fmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
   __syncthreads();
   amax = 0.f;
-  for (int w = 0; w < (int)blockDim.x / 32; w++) amax = fmaxf(amax, warp_max[w]);
-  const float scale = fmaxf(b8::scale_of(amax), old);
+  for (int w = 0; w < (int)blockDim.x / 32; w++) amax = fmax_nan(amax, warp_max[w]);
+  const float scale = fmax_nan(b8::scale_of(amax), old);
   const float inv = b8::inverse(scale);
 
   if (KEEP) {

@@ -467,8 +467,9 @@ KVQ_API kvq_status kvq_rope(const kvq_rope_spec *spec, kvq_dtype dtype, int32_t 
  * rotation is applied, so any head_dim of 64, 128 or 256 serves.
  *   k_codes / v_codes   [num_blocks][num_kv_heads][block_size][head_dim] int8,
  *                       16-byte aligned;
- *   k_scales / v_scales [num_blocks][num_kv_heads] fp32, finite and >= 0; a
- *                       block whose scale is 0 holds zero codes.
+ *   k_scales / v_scales [num_blocks][num_kv_heads] fp32, finite and >= 0, or NaN
+ *                       where an append met an infinity or NaN; a block whose
+ *                       scale is 0 holds zero codes.
  * Token t of sequence b lies in block block_table[b][t / block_size] at row
  * t % block_size.  Table entries outside [0, num_blocks) are unmapped: appends
  * skip them, reads give zeros and attention leaves their tokens out. */
@@ -502,7 +503,9 @@ typedef struct {
  * start_pos[b], 0 otherwise: scale = max(amax / 127, old); codes are
  * rint(x * (1 / scale)) in [-127, 127]; where the scale grew, the codes of the
  * block's earlier tokens become rint(code * (old / scale)).  All in fp32,
- * rounding to nearest even.  Rows behind the new tokens stay as they were.  A
+ * rounding to nearest even.  An infinity or NaN among a block's new elements makes
+ * its scale NaN, and so every value of the block, also of tokens appended to it
+ * before and after.  Rows behind the new tokens stay as they were.  A
  * block must not be reached twice in one call, by two sequences or by one. */
 KVQ_API kvq_status kvq_b8_append(const kvq_b8_cache *cache, const kvq_heads *k,
                                  const kvq_heads *v, kvq_dtype dtype, int32_t batch,

@@ -292,6 +292,38 @@ def test_append_skips_unmapped_blocks_and_tails():
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dim,block,t_new", [(64, 16, 40), (256, 256, 300)])
+@pytest.mark.parametrize("bad", [math.nan, -math.nan, math.inf, -math.inf])
+def test_append_of_what_is_not_finite(dtype, dim, block, t_new, bad):
+    """One element of one head: its block becomes NaN, the others stay as they are,
+    later tokens of the block do not bring it back, and a new start does."""
+    c, d = (kvq.B8Cache.contiguous(1, 2, 600, dim, block) for _ in "cd")
+    k, v = rand(191, 1, t_new, 2, dim, dtype=dtype), rand(192, 1, t_new, 2, dim, dtype=dtype)
+    kvq.b8_append(d, k, v, ints([0]))
+    at = block + 3
+    for which in "kv":
+        x = {"k": k, "v": v}
+        x[which] = x[which].clone()
+        x[which][0, at, 1, dim - 5] = bad
+        kvq.b8_append(c, x["k"], x["v"], ints([0]))
+        for w, got, want in (("k", c.k_scales, d.k_scales), ("v", c.v_scales, d.v_scales)):
+            want = want.clone()
+            if w == which:
+                want[1, 1] = math.nan
+            assert torch.equal(got.isnan(), want.isnan())
+            assert torch.equal(got.nan_to_num(), want.nan_to_num())
+        one = torch.ones((1, 1, 2, dim), dtype=dtype, device="cuda")
+        kvq.b8_append(c, one, one, ints([block + 8]))
+        assert (c.k_scales if which == "k" else c.v_scales)[1, 1].isnan()
+        val = kvq.b8_gather(c, ints([0]), ints([t_new]), t_new, F32)[which == "v"]
+        assert val[0, block:2 * block, 1].isnan().all() and val.isnan().sum() == dim * min(
+            block, t_new - block)
+    kvq.b8_append(c, k, v, ints([0]))
+    assert torch.equal(c.k_scales, d.k_scales) and torch.equal(c.v_scales, d.v_scales)
+    assert torch.equal(c.k_codes, d.k_codes) and torch.equal(c.v_codes, d.v_codes)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_gather_into_16_byte_alignment(dtype):
     c, _ = filled(61, [50, 70], 2, 128, 32)
     first, ends = ints([3, 0]), ints([50, 66])
