@@ -290,20 +290,20 @@ __global__ void __launch_bounds__(512)
         const int hi = max((int)(int16_t)top, (int)top >> 16);
         const int lo = min((int)(int16_t)low, (int)low >> 16);
         const int m = max(hi, -lo);
-        amax[p] = fmaxf(amax[p], __fmul_rn((float)m, sc));
+        amax[p] = fmax_nan(amax[p], __fmul_rn((float)m, sc));
       }
 #pragma unroll
     for (int p = 0; p < 2; p++)
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
-        amax[p] = fmaxf(amax[p], __shfl_xor_sync(0xffffffffu, amax[p], o));
+        amax[p] = fmax_nan(amax[p], __shfl_xor_sync(0xffffffffu, amax[p], o));
     if (runs > 1) {
       // two sets, so that one barrier a unit is enough
       if (lane == 0) warp_max[parity][0][warp] = amax[0], warp_max[parity][1][warp] = amax[1];
       __syncthreads();
       for (int w = 0; w < runs; w++) {
-        amax[0] = fmaxf(amax[0], warp_max[parity][0][w]);
-        amax[1] = fmaxf(amax[1], warp_max[parity][1][w]);
+        amax[0] = fmax_nan(amax[0], warp_max[parity][0][w]);
+        amax[1] = fmax_nan(amax[1], warp_max[parity][1][w]);
       }
     }
     // a block without kept tokens, or one that is not mapped, is left alone

@@ -780,6 +780,28 @@ def test_evict_long_and_equal_weights():
     assert (wide[..., :keep] == 0.25).all() and (wide[..., keep:] == 0).all()
 
 
+@pytest.mark.parametrize("dim,block,to_block", [(64, 16, 32), (128, 32, 16), (256, 256, 256)])
+def test_evict_carries_nan_along(dim, block, to_block):
+    """A block of a NaN scale: where one of its tokens is kept, the block that it comes
+    to is NaN; where none is, nothing of it is left."""
+    n, keep = 3 * block, 2 * block
+    c, _ = filled(193, [n], 2, dim, block)
+    into, _ = filled(194, [keep], 2, dim, to_block)
+    page = c.block_table[0].long()
+    c.k_scales[page[1], 0] = math.nan
+    c.v_scales[page[2], 1] = math.nan
+    m = torch.ones((1, 2, n), device="cuda")
+    m[0, 0, block + 1:2 * block] = 0.0  # one token of K's block stays
+    m[0, 1, 2 * block:] = 0.0           # none of V's
+    _, kept, _ = kvq.b8_evict(c, into, m, ints([n]), n, keep)
+    k, v = kvq.b8_gather(into, ints([0]), ints([keep]), keep, F32)
+    at = kept[0, 0].tolist().index(block)
+    one = torch.zeros(keep, dtype=torch.bool, device="cuda")
+    one[at // to_block * to_block:(at // to_block + 1) * to_block] = True
+    assert torch.equal(k[0, :, 0].isnan().all(-1), one) and torch.equal(k[0, :, 0].isnan().any(-1), one)
+    assert not k[:, :, 1].isnan().any() and not v.isnan().any()
+
+
 @pytest.mark.parametrize("keep", [64, 40])
 def test_evicted_tokens_without_a_block_become_zeros(keep):
     """Left out by attention before, rows of zeros of score 0 afterwards, whether
