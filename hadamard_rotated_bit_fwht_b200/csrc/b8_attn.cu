@@ -303,9 +303,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, HILO>::kCtas)
 #pragma unroll
     for (int nb = 0; nb < kNb; nb++) {
       // (finite: a product past 2^127 would meet weights below 2^-113 alone, and
-      // 0 * inf would be NaN)
+      // 0 * inf would be NaN; rows that see nothing of the tile take nothing of a NaN)
       float vf = kv.y * vinv[nb];
-      vf = vf > 0x1p127f ? 0x1p127f : vf;
+      vf = vf > 0x1p127f ? 0x1p127f : (nb ? lim1 : lim0) > tok ? vf : 0.f;
 #pragma unroll
       for (int n = 0; n < 2; n++) {
         const float e0 = ex2(p[nb][2 * n] - m[nb]), e1 = ex2(p[nb][2 * n + 1] - m[nb]);

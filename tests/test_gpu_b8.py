@@ -590,6 +590,28 @@ def test_scales_near_the_ends_of_fp32(dtype, nq):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("block,nq,group,last", [(16, 3, 1, 1), (16, 20, 2, 7), (64, 70, 4, 5),
+                                                 (16, 140, 1, 16), (32, 40, 8, 30)])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_a_bad_block_spoils_the_rows_that_see_it_only(dtype, block, nq, group, last, which):
+    """The last block, of `last` tokens, holds NaN; the first queries end before it."""
+    n = 10 * block + last
+    c, _ = filled(195, [n], 1, 128, block)
+    q = rand(196, nq, group, 128, dtype=dtype)
+    kw = dict(cu_q=ints([0, nq]), max_q=nq)
+    m = [torch.zeros((1, 1, n), device="cuda") for _ in range(2)]
+    want, wlse = kvq.b8_attn(c, q, ints([n]), n, 0.1, return_lse=True, **kw)
+    kvq.b8_attn_mass(c, q, wlse, ints([n]), n, 0.1, m[0], **kw)
+    (c.k_scales if which == "k" else c.v_scales)[c.block_table[0, -1].long()] = math.nan
+    out, lse = kvq.b8_attn(c, q, ints([n]), n, 0.1, return_lse=True, **kw)
+    kvq.b8_attn_mass(c, q, wlse, ints([n]), n, 0.1, m[1], **kw)
+    sees = nq - last
+    assert torch.equal(out[:sees], want[:sees]) and torch.equal(lse[:sees], wlse[:sees])
+    assert torch.isnan(out[sees:]).all()
+    assert torch.equal(m[0][..., :n - last], m[1][..., :n - last])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("scale", [0.0, -0.125])
 def test_other_scales(dtype, scale):
     c, _ = filled(73, [300, 40], 1, 64, 32)
