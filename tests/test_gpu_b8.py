@@ -1054,6 +1054,59 @@ def test_streams_graphs_and_workspaces():
         assert torch.equal(o, want)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("nq", [1, 5, 150])
+def test_a_captured_step(dtype, nq):
+    """Rotate, append, attend, add up the weights, evict and read back in one graph,
+    over inputs that change between replays: as the eager calls, bit by bit."""
+    B, hq, hkv, dim, bs, room, keep = 3, 8, 2, 64, 16, 640, 200
+    r = kvq.Rope.make(dim)
+
+    def state(seed):
+        c, _ = filled(seed, [room] * B, hkv, dim, bs)
+        into, _ = filled(seed + 1, [keep] * B, hkv, dim, bs)
+        x = rand(seed + 2, B * nq, hq + 2 * hkv, dim, dtype=dtype)
+        lens = ints([seed % 300 + nq, 7 + nq, 450])
+        return [c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.block_table, into.k_codes,
+                into.k_scales, into.v_codes, into.v_scales, into.block_table, x, lens]
+
+    def step(s):
+        c, into = kvq.B8Cache.wrap(*s[:5]), kvq.B8Cache.wrap(*s[5:10])
+        x, lens = s[10:]
+        cu = torch.arange(0, B * nq + 1, nq, dtype=torch.int32, device="cuda")
+        start = lens - nq
+        pos = (start[:, None] + torch.arange(nq, dtype=torch.int32, device="cuda")).contiguous()
+        kw = dict(cu_q=cu, max_q=nq) if nq > 1 else {}
+        q, _ = kvq.rope(x[:, :hq], None, pos.view(-1), r)
+        kv = x.view(B, nq, hq + 2 * hkv, dim)
+        kvq.b8_append(c, kv[:, :, hq:hq + hkv], kv[:, :, hq + hkv:], start, rope=r)
+        out, lse = kvq.b8_attn(c, q, lens, room, 0.125, return_lse=True, **kw)
+        m = torch.zeros((B, hkv, room), device="cuda")
+        kvq.b8_attn_mass(c, q, lse, lens, room, 0.125, m, **kw)
+        ev = kvq.b8_evict(c, into, m, lens, room, keep, recent=20, sinks=2)
+        return (out, lse, m, *ev, *kvq.b8_gather(into, torch.zeros_like(lens), ev[0], keep, dtype))
+
+    seeds = (201, 305, 411)
+    want = [[t.clone() for t in step(state(s))] for s in seeds]
+    held = state(seeds[0])
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        step(held)
+        st.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=st):
+            got = step(held)
+        for seed, w in zip(seeds, want):
+            for t, new in zip(held, state(seed)):
+                t.copy_(new)
+            gr.replay()
+            gr.replay()  # the same tokens again, over their own codes
+            st.synchronize()
+            for i, (a, b) in enumerate(zip(got, w)):
+                assert torch.equal(a, b), i
+
+
 def test_refusals_on_the_device():
     c, _ = filled(141, [64], 1, 64, 16)
     q = rand(142, 1, 2, 64)
