@@ -26,9 +26,11 @@ cudaError_t allow_smem(int bytes) {
 // Launch that may begin while the kernel before it on the stream ends; cluster:
 // CTAs of a cluster (1: none).  Every thread of f starts with
 // dec::grid_dependency_wait(): it waits until that kernel is done and its writes
-// are visible, so stream order is kept and only the launch itself overlaps.  What such kernels read they read past
-// L1 (__ldcg, cp.async.cg) or with plain loads, not through the read-only path,
-// whose data must not change while a grid exists.
+// are visible, so stream order is kept and only the launch itself overlaps.  What
+// such kernels read they read past L1 (__ldcg, cp.async.cg) or with plain loads, not
+// through the read-only path, whose data must not change while a grid exists.  Block
+// scales come through L1 (cp.async.ca, as 4 bytes must): a kernel that writes them
+// has to end before its dependents may begin, as those here do.
 template <class... P, class... A>
 cudaError_t launch_early(void (*f)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
                          int cluster, A... args) {

@@ -7,9 +7,9 @@
 // has one owner, and the sum's order depends on the sizes alone.  Rows come in
 // chunks of up to kChunk staged in shared memory; every chunk walks the CTA's
 // tokens, which then come from L2.  Bound for a few rows: the K codes from HBM.
-// 32 sequences of 2048 to 16384 tokens, 8 kv heads, D 128, one query each: 69
+// 32 sequences of 2048 to 16384 tokens, 8 kv heads, D 128, one query each: 70
 // us, 4.6 TB/s (71 % of a plain copy; issue slots 51 % used, uneven ends).  The
-// last 32 queries of 4 prompts (128 rows): 37 us, a fourth of it the staging of
+// last 32 queries of 4 prompts (128 rows): 35 us, a fourth of it the staging of
 // the rows, the rest latency at 16 warps an SM (40 us with 16 tokens a step, whose
 // query fragments are read from shared memory twice as often).
 #include "b8_mma.cuh"

@@ -23,11 +23,13 @@
 // their p' from l.
 // Bound: the chain scores -> softmax -> products of a row tile; two tiles take
 // turns on the tensor pipe.  4 prompts of 572 to 778 queries, 32 heads on 8 kv
-// heads, D 128, 6516 to 8075 tokens: 385 us, 795 TFLOP/s (48 % of a cuBLAS bf16
+// heads, D 128, 6516 to 8075 tokens: 387 us, 792 TFLOP/s (48 % of a cuBLAS bf16
 // product).  A tile's 16 products take about 2000 cycles from the first to the
 // last where their operations are 1024, V's layout (dims as rows or as columns)
 // aside; descriptors by constant steps, the wait for V in front of that for the
-// probabilities and no masks for rows of no query brought 410 to 385.  At 410 it
+// probabilities and no masks for rows of no query brought 410 to 383 (units of the
+// largest V scale that a CTA had met saved 4 us of 387, and lost rows on blocks of
+// far smaller ones).  At 410 it
 // took as long without exp2, or without the stores of P; 354 with next to no
 // softmax, 383 with half of the score products, 379 without the conversion.
 // Tiles of 64 tokens with two score buffers a row tile took 660 us (their
@@ -551,7 +553,8 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
         mx = fmaxf(mx, group_max(s[gr / 2] + 16 * (gr & 1), in + gr, inv, cut, lim - tok - 16 * gr));
       // (with the tile's largest V scale in the place of each group's: a bound)
       if (__any_sync(0xffffffffu, mx > ve + 14.f - in[24])) {
-        // the bound serves where the tile's V scales are no more than 4 apart
+        // the bound serves where the tile's V scales are no more than 4 apart (a
+        // maximum over the groups every time: 398 us instead of 387)
         float mvx = mx + in[24];
         if (!(in[24] - in[25] <= 2.f)) {
           mvx = -INFINITY;

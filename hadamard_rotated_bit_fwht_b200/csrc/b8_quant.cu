@@ -11,7 +11,7 @@
 // read and rotated a second time.
 //
 // Prompts of 8 sequences (197 thousand rows of 256 dims of K and of V, bf16, K
-// rotated, blocks of 64): append 108 us, 303 MB; issue slots 62 % used, the
+// rotated, blocks of 64): append 109 us, 303 MB; issue slots 63 % used, the
 // angles a third of them (49 us at a plain copy's rate).  Read back: 51 us, 5.9
 // TB/s, two thirds of it stores.  One token in each of 64 sequences: 5.5 us and
 // 4.4 us, launches and chains of dependent loads.

@@ -396,9 +396,10 @@ KVQ_API kvq_status kvq_octave_decode_attn(const kvq_octave_fmt *fmt, const void 
  * t = position * inv_freq[i] radians,
  *   a' = (a cos t - b sin t) * factor,   b' = (b cos t + a sin t) * factor,
  * with (a, b) = dims (2i, 2i + 1) if interleaved, (i, i + rot_dim / 2)
- * otherwise; dims from rot_dim on are copied.  Angles are formed in fp64 and
- * reduced to one turn there, so far positions lose nothing; the rotation is
- * fp32, rounded once to the output type. */
+ * otherwise; dims from rot_dim on are copied.  A frequency becomes an integer
+ * of 2^-64 turns per position (from fp64, off by 2^-52 of itself), so the angle
+ * of any position wraps exactly; sine and cosine are fp32 series within an eighth
+ * of a turn (2^-23), and the rotation is fp32, rounded once to the output type. */
 typedef struct {
   const double *d_inv_freq; /* device, rot_dim / 2 values, radians per position */
   int32_t rot_dim;          /* a multiple of 16, at most head_dim */
