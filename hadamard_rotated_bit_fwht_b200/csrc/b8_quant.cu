@@ -274,7 +274,8 @@ static cudaError_t append(const kvq_b8_cache &c, const kvq_heads &k, const kvq_h
                           int threads, int smem, int cols, int t_new,
                           const int32_t *start_pos, const int32_t *new_lens,
                           const kvq_rope_spec &spec, const int32_t *rope_pos, cudaStream_t s) {
-  if (smem > 48 * 1024) {
+  // (48 KB hold the kernel's own few bytes too)
+  if (smem > 32 * 1024) {
     const cudaError_t e = allow_smem<b8_append_kernel<BF16, KEEP>>(kKeep);
     if (e != cudaSuccess) return e;
   }

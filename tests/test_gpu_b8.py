@@ -3,6 +3,9 @@ read back, attention, accumulated weight, eviction) against the plain forms of
 b8_reference.py.  Tolerances follow from the roundings that each call makes
 and are stated where they are used."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -13,6 +16,7 @@ from hadamard_rotated_bit_fwht_b200 import build, kvq
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -245,6 +249,39 @@ def test_append_and_gather(dtype, dim, block, hkv, start, new):
                     t = first[b] + i
                     row = val[:, t].float().to(dt) if 0 <= t < ends[b] else torch.zeros(hkv, dim)
                     assert torch.equal(g[b, i].cpu().float(), row.float())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dim,block", [(64, 256), (128, 128), (256, 64), (256, 256)])
+def test_append_of_every_length(dtype, dim, block):
+    """Each number of new rows has its own share of shared memory: all of them up to
+    a block, as one append and as one of a longer padded batch."""
+    k, v = rand(197, 1, block, 1, dim, dtype=dtype), rand(198, 1, block, 1, dim, dtype=dtype)
+    c, d = (kvq.B8Cache.contiguous(1, 1, block, dim, block) for _ in "cd")
+    for n in range(1, block + 1):
+        kvq.b8_append(c, k[:, :n], v[:, :n], ints([0]))
+        kvq.b8_append(d, k, v, ints([0]), new_lens=ints([n]))
+        assert torch.equal(c.k_scales, d.k_scales) and torch.equal(c.v_scales, d.v_scales), n
+        assert torch.equal(c.k_codes[:, :, :n], d.k_codes[:, :, :n]), n
+        assert torch.equal(c.v_codes[:, :, :n], d.v_codes[:, :, :n]), n
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_append_of_48_kilobytes_first(dtype):
+    """33 to 48 rows of 256 dims take 48 KB of shared memory: as the first call of a
+    process, before a larger one has asked for more than the default."""
+    code = f"""
+import torch
+from hadamard_rotated_bit_fwht_b200 import kvq
+for n in (33, 40, 48):
+    c = kvq.B8Cache.contiguous(1, 1, 64, 256, 64)
+    x = torch.ones((1, n, 1, 256), dtype=torch.{dtype}, device="cuda")
+    kvq.b8_append(c, x, x, torch.zeros(1, dtype=torch.int32, device="cuda"))
+    assert (c.k_codes[0, 0, :n] == 127).all() and not c.k_codes[0, 0, n:].any()
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("inter", [False, True])
