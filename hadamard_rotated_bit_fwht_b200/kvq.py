@@ -617,7 +617,9 @@ class _RopeWithGrad(torch.autograd.Function):
 class B8Cache:
     """Paged int8 cache with one fp32 scale per (block of tokens, kv head):
     planes [num_blocks, kv heads, block_size, dim] and [num_blocks, kv heads],
-    block table [num_seqs, columns] (layout in include/kvq.h)."""
+    block table [num_seqs, columns] (layout in include/kvq.h).  A contiguous
+    int32 table on the planes' device is used as it is, so its changes count; any
+    other is copied."""
 
     def __init__(self, num_blocks, num_kv_heads, block_size, head_dim, block_table,
                  device="cuda"):
